@@ -480,6 +480,181 @@ mp_status mp_adamw_step_fp8(mp_plan* plan, mp_state* state, const mp_gradset* la
                             int32_t last_is_first, const mp_adamw_hparams* hp,
                             const mp_fp8set* fp8, mp_stream stream);
 
+/* ------------------------------------------------------------------------
+ * Losses over vocabulary logits: where a micro-batch's gradient starts.
+ *
+ * Each call reads the logits of `rows` token positions and writes a loss per
+ * row (or per pair) and, if asked, the gradient of the logits -- already
+ * multiplied by the loss scale S and divided by the number of targets, both
+ * read from device memory, so that what the backward pass leaves in the 16-bit
+ * gradient buffers is what mp_accumulate expects (S times the gradient of the
+ * mean over n_i targets) and the same count goes to mp_token_weights_dev or
+ * mp_accumulate_first_counts.
+ *
+ * With z = x / temperature, lse_r = log sum_j exp(z_rj), q_rj = exp(z_rj - lse_r)
+ * and the log-probability of row r's target t: lp_r = z_rt - lse_r.
+ *
+ * Conventions of these calls, besides those at the top:
+ *  - Logits and gradients need the alignment of their element type only; row
+ *    starts on 16 bytes (128 are better) let the vector accesses use whole
+ *    lines.  The other arrays are contiguous, aligned to their element type.
+ *  - A target below 0 (-100 by custom), or a weight of exactly 0, switches its
+ *    row off: the row's logits and other inputs are not used (NaN and inf there
+ *    do no harm), its loss and log-probability are 0 and its gradient row is
+ *    written as zeros.  A target (or a teacher's id) >= vocab cannot be refused
+ *    without a sync: no memory is read there, the row's loss, log-probability
+ *    and gradient are NaN, and the step that they feed is skipped as on an overflow.
+ *  - Logits of -inf (a vocabulary mask) have probability 0.  A row without a
+ *    finite logit, or with +inf or NaN, has no distribution: NaN results.
+ *  - Statistics are held in fp32 with the sums over a row joined in binary64,
+ *    in a fixed order (the same bits on every run); losses are formed in
+ *    binary64 and rounded once; a gradient is formed in fp32 and rounded once
+ *    (round to nearest even) to the logits' type.
+ *  - rows = 0 is allowed and enqueues nothing.
+ *  - The logits must be memory of the current device (else MP_ERR_INVALID).
+ *    Nothing is allocated; the calls may be captured into a graph.
+ * ------------------------------------------------------------------------ */
+
+/* fp32 logits; the 16-bit formats are MP_BF16 and MP_FP16.  Not a format of a plan. */
+#define MP_FP32 2
+
+/* Scratch that the calls may use to split rows over several workgroups when
+ * there are few of them (at most 256); 16-byte aligned. */
+#define MP_LOSS_WORKSPACE_BYTES 65536
+
+/* `rows` rows of `vocab` logits, row r at element r * stride (stride >= vocab
+ * unless rows <= 1; 1 <= vocab <= 2^30; rows < 2^22).  temperature: from
+ * 2^-20 to 2^20.  workspace: NULL, or MP_LOSS_WORKSPACE_BYTES of device memory that no
+ * other work uses while the call runs -- calls in stream order can share one,
+ * calls (or graphs) that may overlap need one each.  It is read only where the
+ * same call wrote it.  Results do not depend on whether it is there beyond the
+ * order of a row's sum. */
+typedef struct {
+    const void* data;
+    int64_t rows;
+    int64_t vocab;
+    int64_t stride;
+    int32_t dtype;          /* MP_BF16, MP_FP16 or MP_FP32 */
+    float temperature;
+    void* workspace;
+} mp_logits;
+
+/* Where the gradient goes: element (r, j) at data + r * stride + j, in the
+ * logits' type, multiplied by scale * (*dev_scale) / (*dev_count).  scale:
+ * finite.  dev_scale (device fp32, e.g. from mp_state_scale_ptr) and dev_count
+ * (device int64, e.g. from mp_target_count) are read when the kernels run;
+ * NULL: 1.  data may be the logits themselves with the same stride (the
+ * gradient replaces them); otherwise the two address ranges must not overlap. */
+typedef struct {
+    void* data;
+    int64_t stride;
+    const float* dev_scale;
+    const int64_t* dev_count;
+    float scale;
+} mp_logits_grad;
+
+/* *count = how many of n targets are >= 0 (n >= 0; both in device memory):
+ * the n_i of a micro-batch ("Accumulate gradients and recompute activations",
+ * "Weight each mean by the targets it represents"). */
+mp_status mp_target_count(int64_t n, const int64_t* targets, int64_t* count, mp_stream stream);
+
+/* logp[r] = lp_r and lse[r] = lse_r (lse may be NULL; 0 for a switched-off row).
+ * targets: rows int64. */
+mp_status mp_token_logprob(const mp_logits* x, const int64_t* targets, float* logp, float* lse,
+                           mp_stream stream);
+
+/* The gradient of sum_r dlogp[r] * lp_r for any dlogp, from the lse of
+ * mp_token_logprob on the same logits:
+ *   dx_rj = scale/T * dlogp[r] * ((j = t) - q_rj).
+ * A row with dlogp[r] == 0 is written as zeros without being read. */
+mp_status mp_token_logprob_grad(const mp_logits* x, const int64_t* targets, const float* lse,
+                                const float* dlogp, const mp_logits_grad* grad, mp_stream stream);
+
+/* Cross-entropy: loss[r] = -w_r lp_r; dx_rj = scale/T * w_r * (q_rj - (j = t)).
+ * weights: rows fp32, NULL: all 1.  grad: NULL for the loss alone. */
+mp_status mp_cross_entropy(const mp_logits* x, const int64_t* targets, const float* weights,
+                           float* loss, const mp_logits_grad* grad, mp_stream stream);
+
+/* Clipped policy loss with a KL penalty.  0 <= clip_low <= 1, clip_high >= 0,
+ * kl_coef >= 0, all finite. */
+typedef struct {
+    float clip_low;
+    float clip_high;
+    float kl_coef;
+} mp_policy_cfg;
+
+/* With rho = exp(lp - old_logp), A = advantage and d = ref_logp - lp:
+ *   kl[r]   = exp(d) - d - 1                       (the estimate of KL(policy || reference))
+ *   loss[r] = w (-min(rho A, clip(rho, 1 - clip_low, 1 + clip_high) A) + kl_coef kl)
+ *   dL/dlp  = w (-rho A where rho A <= clip(rho) A, else 0;  + kl_coef (1 - exp(d)))
+ *   dx_rj   = scale/T * dL/dlp * ((j = t) - q_rj)
+ * On the border of the range the unclipped side is taken.  A = 0 gives a zero
+ * policy term whatever rho is.  old_logp and advantage: rows fp32; ref_logp:
+ * rows fp32, NULL only with kl_coef = 0 (then kl must be NULL); weights: rows
+ * fp32, NULL: all 1.  logp and kl: outputs of rows fp32, each may be NULL.
+ * grad: NULL for the losses alone. */
+mp_status mp_policy_loss(const mp_logits* x, const int64_t* targets, const float* old_logp,
+                         const float* ref_logp, const float* advantage, const float* weights,
+                         const mp_policy_cfg* cfg, float* loss, float* logp, float* kl,
+                         const mp_logits_grad* grad, mp_stream stream);
+
+/* Preference loss of pairs of sequences.  kind MP_PREF_SIGMOID: minus the
+ * smoothed log-sigmoid; MP_PREF_SQUARED: the squared distance to 1/(2 beta).
+ * beta > 0, 0 <= label_smoothing <= 0.5, margin, all finite.  length_mean != 0
+ * takes a sequence's mean log-probability instead of its sum. */
+#define MP_PREF_SIGMOID 0
+#define MP_PREF_SQUARED 1
+typedef struct {
+    int32_t kind;
+    int32_t length_mean;
+    float beta;
+    float label_smoothing;
+    float margin;
+} mp_preference_cfg;
+
+/* n_pairs >= 1 pairs: sequence i (0 <= i < 2 n_pairs) is rows seq_start[i] ..
+ * seq_start[i + 1] - 1, pair p the chosen sequence p and the rejected sequence
+ * n_pairs + p.  seq_start: 2 n_pairs + 1 int64 in device memory, not
+ * decreasing, 0 <= seq_start[i] <= rows (a value outside is taken as the
+ * nearest of these, a sequence that would end before it starts as empty).
+ * With pi_i the sum (mean) of lp over the targets of sequence i -- 0 if it has
+ * none -- and ref_logp[i] the reference's (NULL: 0):
+ *   D = (pi_p - ref_p) - (pi_{p+n} - ref_{p+n});   h = beta D - margin
+ *   loss[p] = -(1 - eps) log sigmoid(h) - eps log sigmoid(-h)     MP_PREF_SIGMOID
+ *   loss[p] = (D - 1/(2 beta))^2                                  MP_PREF_SQUARED
+ * Outputs: loss (n_pairs), seq_logp (2 n_pairs: pi), logp, lse and dlogp (rows
+ * each: dlogp is dloss/dlp, 0 outside every sequence).  Then the gradient of the sum of
+ * the losses goes to grad as in mp_token_logprob_grad (NULL: no gradient). */
+mp_status mp_preference_loss(const mp_logits* x, const int64_t* targets, int64_t n_pairs,
+                             const int64_t* seq_start, const float* ref_logp,
+                             const mp_preference_cfg* cfg, float* loss, float* seq_logp,
+                             float* logp, float* lse, float* dlogp, const mp_logits_grad* grad,
+                             mp_stream stream);
+
+/* A teacher's top k entries of every row (1 <= k <= MP_DISTILL_MAX_K): entry
+ * (r, e) is values[r * k + e], a logit in `dtype`, of vocabulary id
+ * ids[r * k + e].  An id below 0 marks an entry that is not there.  An id may
+ * come twice in a row: its shares add up. */
+#define MP_DISTILL_MAX_K 1024
+typedef struct {
+    const void* values;
+    const int64_t* ids;
+    const float* lse;       /* rows fp32, or NULL */
+    int32_t k;
+    int32_t dtype;          /* MP_BF16, MP_FP16 or MP_FP32 */
+} mp_teacher;
+
+/* Distillation from a teacher's top logits, at the logits' temperature T:
+ *   p_e     = exp(v_e / T - lse_r) with the teacher's own lse_r over its whole
+ *             vocabulary (at T), or the softmax of v / T over the k entries (lse NULL);
+ *   loss[r] = w sum_e p_e (log p_e - log q_{id_e})        (p_e = 0 adds 0)
+ *   dx_rj   = scale/T * w * (q_rj sum_e p_e - sum_{id_e = j} p_e)
+ * The factor T^2 that some apply is the caller's (in weights or scale).  A row
+ * without entries has loss and gradient 0.  weights: rows fp32, NULL: all 1.
+ * grad: NULL for the loss alone. */
+mp_status mp_distill_loss(const mp_logits* x, const mp_teacher* teacher, const float* weights,
+                          float* loss, const mp_logits_grad* grad, mp_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -19,6 +19,7 @@ from .build import LIB as _LIB_PATH
 
 MP_BF16 = 0
 MP_FP16 = 1
+MP_FP32 = 2            # logits only
 
 MP_OK, MP_ERR_INVALID, MP_ERR_ALIGN, MP_ERR_NOMEM, MP_ERR_HIP, MP_ERR_ORDER = range(6)
 
@@ -34,10 +35,15 @@ ENTRY_POINTS = [
     "mp_gradset_update", "mp_update_step", "mp_token_weights_dev", "mp_accumulate_group",
     "mp_update_step_group", "mp_unscale_check_norm_group", "mp_adamw_step_group",
     "mp_norm_partial_group", "mp_update_step_noalloc", "mp_accumulate_first_counts",
+    "mp_target_count", "mp_token_logprob", "mp_token_logprob_grad", "mp_cross_entropy",
+    "mp_policy_loss", "mp_preference_loss", "mp_distill_loss",
 ]
 
 MP_STATE_BLOB_BYTES = 256
 MP_NOALLOC_MAX_NORM_BLOCKS = 262144
+MP_LOSS_WORKSPACE_BYTES = 65536
+MP_DISTILL_MAX_K = 1024
+MP_PREF_SIGMOID, MP_PREF_SQUARED = range(2)
 
 
 class MpError(RuntimeError):
@@ -70,6 +76,34 @@ class Stats(ctypes.Structure):
     def as_dict(self):
         return {name: getattr(self, name) for name, _ in self._fields_
                 if not name.startswith("reserved")}
+
+
+class Logits(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("rows", ctypes.c_int64), ("vocab", ctypes.c_int64),
+                ("stride", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("temperature", ctypes.c_float), ("workspace", ctypes.c_void_p)]
+
+
+class LogitsGrad(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64),
+                ("dev_scale", ctypes.c_void_p), ("dev_count", ctypes.c_void_p),
+                ("scale", ctypes.c_float)]
+
+
+class PolicyCfg(ctypes.Structure):
+    _fields_ = [("clip_low", ctypes.c_float), ("clip_high", ctypes.c_float),
+                ("kl_coef", ctypes.c_float)]
+
+
+class PreferenceCfg(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("length_mean", ctypes.c_int32),
+                ("beta", ctypes.c_float), ("label_smoothing", ctypes.c_float),
+                ("margin", ctypes.c_float)]
+
+
+class Teacher(ctypes.Structure):
+    _fields_ = [("values", ctypes.c_void_p), ("ids", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("k", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
 _lib = None
@@ -132,6 +166,13 @@ def _bind(L):
         "mp_adamw_step_group": ([P, P, PP, P, i32, i32, i32, ctypes.POINTER(AdamWHparams), P],
                                 i32),
         "mp_norm_partial_group": ([P, P, PP, P, i32, i32, i32, P, P], i32),
+        "mp_target_count": ([i64, P, P, P], i32),
+        "mp_token_logprob": ([P, P, P, P, P], i32),
+        "mp_token_logprob_grad": ([P, P, P, P, P, P], i32),
+        "mp_cross_entropy": ([P, P, P, P, P, P], i32),
+        "mp_policy_loss": ([P] * 12, i32),
+        "mp_preference_loss": ([P, P, i64] + [P] * 10, i32),
+        "mp_distill_loss": ([P, P, P, P, P, P], i32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -417,6 +458,166 @@ def mp_fp8set_destroy(fp8set):
 def mp_adamw_step_fp8(plan, state, last, w_last, last_is_first, hp, fp8set, stream=None):
     _check(lib().mp_adamw_step_fp8(plan, state, last, float(w_last), int(bool(last_is_first)),
                                    ctypes.byref(hp), fp8set, _stream(stream)))
+
+
+# --- losses over vocabulary logits ----------------------------------------------
+
+_LOGITS_DTYPE = {torch.bfloat16: MP_BF16, torch.float16: MP_FP16, torch.float32: MP_FP32}
+
+
+def _array(x, dtype, n, name, device=None):
+    """Device address of a contiguous array of at least n elements: a tensor (checked) or an
+    int address; None stays NULL."""
+    if x is None or isinstance(x, int):
+        return x
+    if x.dtype != dtype:
+        raise TypeError("%s must be a %s tensor, not %s" % (name, dtype, x.dtype))
+    if x.numel() < n or not x.is_contiguous():
+        raise ValueError("%s must be contiguous, with %d elements" % (name, n))
+    if x.device.type != "cuda" or (device is not None and x.device != device):
+        raise ValueError("%s must be on the logits' GPU" % name)
+    return x.data_ptr()
+
+
+def _matrix(x, name):
+    if x.dim() != 2 or x.dtype not in _LOGITS_DTYPE:
+        raise TypeError("%s must be a 2-D bfloat16, float16 or float32 tensor" % name)
+    if x.device.type != "cuda":
+        raise ValueError("%s must be on a GPU" % name)
+    if x.shape[1] > 1 and x.stride(1) != 1:
+        raise ValueError("%s: the elements of a row must be adjacent" % name)
+    return x.data_ptr(), x.shape[0], x.shape[1], x.stride(0) if x.shape[0] > 1 else x.shape[1]
+
+
+def logits(x, temperature=1.0, workspace=None):
+    """The mp_logits of a 2-D tensor [rows, vocab] (rows may be strided).  workspace: a tensor of
+    MP_LOSS_WORKSPACE_BYTES uint8 on its GPU, used where there are few rows.  The struct holds
+    addresses: keep the tensors alive while work that uses them is enqueued."""
+    data, rows, vocab, stride = _matrix(x, "logits")
+    w = _array(workspace, torch.uint8, MP_LOSS_WORKSPACE_BYTES, "workspace", x.device)
+    out = Logits(data, rows, vocab, stride, _LOGITS_DTYPE[x.dtype], temperature, w)
+    out.torch = (x.dtype, x.device)
+    return out
+
+
+def logits_grad(dx, scale=1.0, dev_scale=None, dev_count=None):
+    """The mp_logits_grad that writes to the 2-D tensor dx: the gradient times scale * dev_scale /
+    dev_count.  dev_scale: a float32 tensor or the address mp_state_scale_ptr gives; dev_count: an
+    int64 tensor (mp_target_count)."""
+    data, rows, vocab, stride = _matrix(dx, "the gradient")
+    out = LogitsGrad(data, stride, _array(dev_scale, torch.float32, 1, "dev_scale", dx.device),
+                     _array(dev_count, torch.int64, 1, "dev_count", dx.device), scale)
+    out.torch = (dx.dtype, dx.device, rows, vocab)
+    return out
+
+
+def policy_cfg(clip_low=0.2, clip_high=0.2, kl_coef=0.0):
+    return PolicyCfg(clip_low, clip_high, kl_coef)
+
+
+def preference_cfg(kind=MP_PREF_SIGMOID, beta=0.1, label_smoothing=0.0, margin=0.0,
+                   length_mean=False):
+    return PreferenceCfg(kind, int(bool(length_mean)), beta, label_smoothing, margin)
+
+
+def teacher(values, ids, lse=None):
+    """The mp_teacher of two contiguous [rows, k] tensors: logits (bf16, fp16 or fp32) and int64
+    ids; lse: rows float32, the teacher's own normaliser at the student's temperature."""
+    if values.dim() != 2 or values.dtype not in _LOGITS_DTYPE:
+        raise TypeError("teacher values must be a 2-D bfloat16, float16 or float32 tensor")
+    if ids.shape != values.shape:
+        raise ValueError("teacher values and ids must have the same shape")
+    rows, k = values.shape
+    out = Teacher(_array(values, values.dtype, rows * k, "teacher values"),
+                  _array(ids, torch.int64, rows * k, "teacher ids", values.device),
+                  _array(lse, torch.float32, rows, "teacher lse", values.device), k,
+                  _LOGITS_DTYPE[values.dtype])
+    out.torch = (values.device, rows)
+    return out
+
+
+def _grad_of(x, grad):
+    """byref of a gradient that fits the logits x; None stays NULL."""
+    if grad is None:
+        return None
+    t = getattr(grad, "torch", None)
+    if t is not None and hasattr(x, "torch"):
+        if t[:2] != x.torch:
+            raise TypeError("the gradient must have the logits' type and GPU")
+        if t[2:] != (x.rows, x.vocab):
+            raise ValueError("the gradient must have the logits' shape")
+    return ctypes.byref(grad)
+
+
+def _rows_of(x):
+    """A checker of per-row arrays for the logits x."""
+    device = x.torch[1] if hasattr(x, "torch") else None
+    return lambda a, dtype, name, n=x.rows: _array(a, dtype, n, name, device)
+
+
+def mp_target_count(targets, count, n=None, stream=None):
+    """count[0] = how many targets (int64, the first n or all) are >= 0."""
+    n = targets.numel() if n is None else int(n)
+    _check(lib().mp_target_count(n, _array(targets, torch.int64, n, "targets"),
+                                 _array(count, torch.int64, 1, "count"), _stream(stream)))
+
+
+def mp_token_logprob(x, targets, logp, lse=None, stream=None):
+    """x: logits(...); targets: int64 [rows]; logp and lse: float32 [rows], written."""
+    f = _rows_of(x)
+    _check(lib().mp_token_logprob(ctypes.byref(x), f(targets, torch.int64, "targets"),
+                                  f(logp, torch.float32, "logp"), f(lse, torch.float32, "lse"),
+                                  _stream(stream)))
+
+
+def mp_token_logprob_grad(x, targets, lse, dlogp, grad, stream=None):
+    f = _rows_of(x)
+    _check(lib().mp_token_logprob_grad(ctypes.byref(x), f(targets, torch.int64, "targets"),
+                                       f(lse, torch.float32, "lse"),
+                                       f(dlogp, torch.float32, "dlogp"), _grad_of(x, grad),
+                                       _stream(stream)))
+
+
+def mp_cross_entropy(x, targets, weights, loss, grad=None, stream=None):
+    f = _rows_of(x)
+    _check(lib().mp_cross_entropy(ctypes.byref(x), f(targets, torch.int64, "targets"),
+                                  f(weights, torch.float32, "weights"),
+                                  f(loss, torch.float32, "loss"), _grad_of(x, grad),
+                                  _stream(stream)))
+
+
+def mp_policy_loss(x, targets, old_logp, ref_logp, advantage, weights, cfg, loss, logp=None,
+                   kl=None, grad=None, stream=None):
+    f, t = _rows_of(x), torch.float32
+    _check(lib().mp_policy_loss(ctypes.byref(x), f(targets, torch.int64, "targets"),
+                                f(old_logp, t, "old_logp"), f(ref_logp, t, "ref_logp"),
+                                f(advantage, t, "advantage"), f(weights, t, "weights"),
+                                ctypes.byref(cfg), f(loss, t, "loss"), f(logp, t, "logp"),
+                                f(kl, t, "kl"), _grad_of(x, grad), _stream(stream)))
+
+
+def mp_preference_loss(x, targets, n_pairs, seq_start, ref_logp, cfg, loss, seq_logp, logp, lse,
+                       dlogp, grad=None, stream=None):
+    f, t, n = _rows_of(x), torch.float32, int(n_pairs)
+    _check(lib().mp_preference_loss(ctypes.byref(x), f(targets, torch.int64, "targets"), n,
+                                    f(seq_start, torch.int64, "seq_start", 2 * n + 1),
+                                    f(ref_logp, t, "ref_logp", 2 * n), ctypes.byref(cfg),
+                                    f(loss, t, "loss", n), f(seq_logp, t, "seq_logp", 2 * n),
+                                    f(logp, t, "logp"), f(lse, t, "lse"), f(dlogp, t, "dlogp"),
+                                    _grad_of(x, grad), _stream(stream)))
+
+
+def mp_distill_loss(x, teacher, weights, loss, grad=None, stream=None):
+    f = _rows_of(x)
+    if hasattr(teacher, "torch") and hasattr(x, "torch"):
+        if teacher.torch[0] != x.torch[1]:
+            raise ValueError("the teacher's entries must be on the logits' GPU")
+        if teacher.torch[1] < x.rows:
+            raise ValueError("the teacher must have an entry list for each of %d rows" % x.rows)
+    _check(lib().mp_distill_loss(ctypes.byref(x), ctypes.byref(teacher),
+                                 f(weights, torch.float32, "weights"),
+                                 f(loss, torch.float32, "loss"), _grad_of(x, grad),
+                                 _stream(stream)))
 
 
 # --- convenience ---------------------------------------------------------------

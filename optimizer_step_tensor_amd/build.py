@@ -5,7 +5,8 @@ import subprocess
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libmpstep.so")
-SOURCES = [os.path.join(HERE, "csrc", f) for f in ("api.hip", "kernels.hip")]
+SOURCES = [os.path.join(HERE, "csrc", f) for f in ("api.hip", "kernels.hip", "losses_api.hip",
+                                                   "losses.hip")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 # -ffp-contract=off: no fusing of a*b+c, every operation rounds as written.

@@ -11,6 +11,7 @@
 #include <vector>
 
 #include "internal.h"
+#include "losses.h"
 
 using mpk::Chunk;
 using mpk::DevState;
@@ -405,6 +406,26 @@ mp_status make_group(const mp_gradset* const* sets, const float* weights, int32_
 }
 
 }  // namespace
+
+namespace mpk {
+
+// The losses' half of the ABI (losses_api.hip) reports through the same detail text.
+mp_status set_error(mp_status st, const char* fmt, ...)
+{
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    return fail(st, "%s", buf);
+}
+
+mp_status set_ok()
+{
+    return ok();
+}
+
+}  // namespace mpk
 
 extern "C" {
 
