@@ -194,7 +194,8 @@ struct Stat {
     double s;
 };
 
-// Join every lane's share; the result is valid in all lanes of the block.
+// Join every lane's share; the result is valid in the first wave, whose lanes
+// alone go on to the row's formula.
 template <int THREADS>
 __device__ __forceinline__ Stat join(const Acc& a, float k_hi, float k_lo)
 {
@@ -204,7 +205,7 @@ __device__ __forceinline__ Stat join(const Acc& a, float k_hi, float k_lo)
     float m = a.m;
 #pragma unroll
     for (int d = 1; d < kWave; d <<= 1) m = __builtin_fmaxf(m, __shfl_xor(m, d));
-    double s = static_cast<double>(a.s) * exp2_hw(scaled(a.m, m, k_hi, k_lo));
+    double s = static_cast<double>(a.s * exp2_hw(scaled(a.m, m, k_hi, k_lo)));
 #pragma unroll
     for (int d = 1; d < kWave; d <<= 1) s += __shfl_xor(s, d);
     if constexpr (W == 1) return Stat{m, s};
@@ -214,12 +215,16 @@ __device__ __forceinline__ Stat join(const Acc& a, float k_hi, float k_lo)
         ss[wave] = s;
     }
     __syncthreads();
+    if (wave != 0) return Stat{m, s};
+    m = sm[lane % W];
+    s = ss[lane % W];
+    float top = m;
 #pragma unroll
-    for (int i = 0; i < W; ++i) m = __builtin_fmaxf(m, sm[i]);
-    s = 0.0;
+    for (int d = 1; d < W; d <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, d));
+    s *= exp2_hw(scaled(m, top, k_hi, k_lo));
 #pragma unroll
-    for (int i = 0; i < W; ++i) s += ss[i] * exp2_hw(scaled(sm[i], m, k_hi, k_lo));
-    return Stat{m, s};
+    for (int d = 1; d < W; d <<= 1) s += __shfl_xor(s, d);
+    return Stat{top, s};
 }
 
 // Sum of one double per lane, valid in all lanes.  Shared memory of its own.
@@ -441,7 +446,56 @@ __device__ __forceinline__ void store_shares(const TeacherRow& t, int k, typenam
     }
 }
 
-// One row per workgroup; the row is read a second time for the gradient.
+// What the first wave tells the others: dx_j = c exp2((x_j - m) k), and the
+// value of the target's element (or the factor of a teacher's share).
+struct RowGrad {
+    float m, c, fix;
+};
+
+// The row's loss from its statistics: the outputs are written and the gradient's
+// numbers broadcast.  Only the first wave holds st; all lanes return the same.
+template <int DT, int THREADS, bool DISTILL>
+__device__ __forceinline__ RowGrad row_formula(const LossArgs& a, int64_t row, const Stat& st, double w,
+                                               int64_t target, float xt, const TeacherRow& t)
+{
+    __shared__ RowGrad out;
+    if (threadIdx.x < kWave) {
+        const double ln_s = log_sum(st.s);
+        const double lse = static_cast<double>(st.m) * a.x.inv_t + ln_s;
+        const double factor = a.g.dx != nullptr ? grad_factor(a.g) : 0.0;
+        double mult, fix;
+        if constexpr (DISTILL) {
+            if (threadIdx.x == 0) a.loss[row] = static_cast<float>(w * (t.cross + t.mass * lse));
+            fix = factor * w;
+            mult = fix * t.mass;
+        } else {
+            const double lp = (static_cast<double>(xt) - static_cast<double>(st.m)) * a.x.inv_t - ln_s;
+            mult = -factor * target_loss(a, row, w, lp, lse, threadIdx.x == 0);
+            if (target >= a.x.vocab) mult = __builtin_nan("");
+            fix = mult * expm1(lp);
+        }
+        if (threadIdx.x == 0)
+            out = RowGrad{st.m, static_cast<float>(mult / st.s), static_cast<float>(fix)};
+    }
+    __syncthreads();      // also: the logits that are needed singly are read, in place is fine
+    return out;
+}
+
+// The elements that differ from the dense gradient, after all of it is stored.
+template <int DT, int THREADS, bool DISTILL>
+__device__ __forceinline__ void store_exceptions(const LossArgs& a, const TeacherRow& t, int64_t target,
+                                                 typename Fmt<DT>::T* dx, const RowGrad& r)
+{
+    __syncthreads();
+    if constexpr (DISTILL) {
+        store_shares<DT, THREADS>(t, a.k, dx, r.m, a.x.k_hi, a.x.k_lo, r.c, r.fix);
+    } else {
+        if (threadIdx.x == 0 && target < a.x.vocab) store_one<DT>(dx + target, r.fix);
+    }
+}
+
+// One row per workgroup, any length; the row is read a second time for the
+// gradient.
 template <int DT, int THREADS, bool DISTILL>
 __global__ __launch_bounds__(THREADS) void k_rows(LossArgs a)
 {
@@ -461,6 +515,7 @@ __global__ __launch_bounds__(THREADS) void k_rows(LossArgs a)
         t = teacher_row<DT, THREADS>(a, row, x, lds);
         if (t.mass == 0.0) return off_row<DT, THREADS>(a, row, dx);
     }
+    const float xt = DISTILL ? 0.0f : target < n ? widen<DT>(x[target]) : __builtin_nanf("");
 
     const float k_hi = a.x.k_hi, k_lo = a.x.k_lo;
     const Span<DT> sp(dx != nullptr ? static_cast<const void*>(dx) : x, n);
@@ -478,39 +533,88 @@ __global__ __launch_bounds__(THREADS) void k_rows(LossArgs a)
         add(acc, f, k_hi, k_lo);
     }
     const Stat st = join<THREADS>(acc, k_hi, k_lo);
-    const double ln_s = log_sum(st.s);
-    const double lse = static_cast<double>(st.m) * a.x.inv_t + ln_s;
-
-    const double factor = dx != nullptr ? grad_factor(a.g) : 0.0;
-    double mult, fix;                   // dx_j = mult q_j; the target's element, or a share's factor
-    if constexpr (DISTILL) {
-        if (tid == 0) a.loss[row] = static_cast<float>(w * (t.cross + t.mass * lse));
-        fix = factor * w;
-        mult = fix * t.mass;
-    } else {
-        const float xt = target < n ? widen<DT>(x[target]) : __builtin_nanf("");
-        const double lp = (static_cast<double>(xt) - static_cast<double>(st.m)) * a.x.inv_t - ln_s;
-        mult = -factor * target_loss(a, row, w, lp, lse, tid == 0);
-        if (target >= n) mult = __builtin_nan("");
-        fix = mult * expm1(lp);
-    }
+    const RowGrad r = row_formula<DT, THREADS, DISTILL>(a, row, st, w, target, xt, t);
     if (dx == nullptr) return;
-    __syncthreads();                    // the logits that are needed singly are read: in place is fine
-    const float c = static_cast<float>(mult / st.s);
     for (int i = tid; i < sp.nvec; i += THREADS) {
         float f[E];
         unpack<DT>(load_vec<DT>(x + sp.head + i * E), f);
 #pragma unroll
-        for (int j = 0; j < E; ++j) f[j] = share_of<DT>(f[j], st.m, k_hi, k_lo) * c;
+        for (int j = 0; j < E; ++j) f[j] = share_of<DT>(f[j], r.m, k_hi, k_lo) * r.c;
         store_vec<DT>(dx + sp.head + i * E, pack<DT>(f));
     }
-    if (one >= 0) store_one<DT>(dx + one, share_of<DT>(single, st.m, k_hi, k_lo) * c);
-    __syncthreads();                    // the dense gradient is stored before the elements over it
-    if constexpr (DISTILL) {
-        store_shares<DT, THREADS>(t, a.k, dx, st.m, k_hi, k_lo, c, static_cast<float>(fix));
-    } else {
-        if (tid == 0 && target < n) store_one<DT>(dx + target, static_cast<float>(fix));
+    if (one >= 0) store_one<DT>(dx + one, share_of<DT>(single, r.m, k_hi, k_lo) * r.c);
+    store_exceptions<DT, THREADS, DISTILL>(a, t, target, dx, r);
+}
+
+// One row per workgroup, held in registers between the statistics and the
+// gradient: NV vectors a lane, the first FULL of them inside the row for every
+// lane, all requested before the first is used.
+template <int DT, int THREADS, int NV, int FULL, bool DISTILL>
+__global__ __launch_bounds__(THREADS) void k_rows_held(LossArgs a)
+{
+    using T = typename Fmt<DT>::T;
+    constexpr int E = Fmt<DT>::E;
+    extern __shared__ char lds[];
+    const int64_t row = blockIdx.x;
+    const int tid = threadIdx.x;
+    const int n = a.x.vocab;
+    const T* x = static_cast<const T*>(a.x.x) + row * a.x.stride;
+    T* dx = static_cast<T*>(a.g.dx) + row * a.g.stride;
+    const int64_t target = DISTILL ? 0 : read_table(a.targets + row);
+    const double w = a.weights != nullptr ? static_cast<double>(read_table(a.weights + row)) : 1.0;
+    if (target < 0 || w == 0.0) return off_row<DT, THREADS>(a, row, dx);
+
+    const float k_hi = a.x.k_hi, k_lo = a.x.k_lo;
+    const Span<DT> sp(dx, n);
+    // lanes past the end take the last vector once more, and drop it when it is used
+    u32x4 v[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int e = i * THREADS + tid;
+        v[i] = load_vec<DT>(x + sp.head + (i < FULL ? e : min(e, sp.nvec - 1)) * E);
     }
+    const int one = sp.single(tid);
+    float single = one >= 0 ? widen<DT>(x[one]) : -__builtin_inff();
+    const float xt = DISTILL ? 0.0f : target < n ? widen<DT>(x[target]) : __builtin_nanf("");
+    TeacherRow t;
+    if constexpr (DISTILL) {
+        t = teacher_row<DT, THREADS>(a, row, x, lds);
+        if (t.mass == 0.0) return off_row<DT, THREADS>(a, row, dx);
+    }
+    Acc acc;
+#pragma unroll
+    for (int i = 0; i < NV; i += 2) {
+        float f[2 * E];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float g[E];
+            unpack<DT>(v[i + h], g);
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+                f[h * E + j] = i + h < FULL || (i + h) * THREADS + tid < sp.nvec ? g[j]
+                                                                             : -__builtin_inff();
+        }
+        add(acc, f, k_hi, k_lo);
+        // the gradient unpacks the vectors again: kept unpacked, they would take twice the registers
+        asm("" : "+v"(v[i]), "+v"(v[i + 1]));
+    }
+    {
+        const float f[1] = {single};
+        add(acc, f, k_hi, k_lo);
+    }
+    const Stat st = join<THREADS>(acc, k_hi, k_lo);
+    const RowGrad r = row_formula<DT, THREADS, DISTILL>(a, row, st, w, target, xt, t);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        float f[E];
+        unpack<DT>(v[i], f);
+#pragma unroll
+        for (int j = 0; j < E; ++j) f[j] = share_of<DT>(f[j], r.m, k_hi, k_lo) * r.c;
+        if (i < FULL || i * THREADS + tid < sp.nvec)
+            store_vec<DT>(dx + sp.head + (i * THREADS + tid) * E, pack<DT>(f));
+    }
+    if (one >= 0) store_one<DT>(dx + one, share_of<DT>(single, r.m, k_hi, k_lo) * r.c);
+    store_exceptions<DT, THREADS, DISTILL>(a, t, target, dx, r);
 }
 
 // The gradient of log-probabilities from their lse.  With L = lse log2(e) split
@@ -677,10 +781,36 @@ __global__ __launch_bounds__(kCountThreads) void k_target_count(int64_t n, const
 
 constexpr int kRowThreads = 256;
 
+template <int DT, int THREADS, int NV, int FULL>
+void held(const LossArgs& a, hipStream_t s)
+{
+    const dim3 grid(static_cast<unsigned>(a.x.rows));
+    if (a.kind == kDistill)
+        k_rows_held<DT, THREADS, NV, FULL, true><<<grid, THREADS, 12u * a.k, s>>>(a);
+    else
+        k_rows_held<DT, THREADS, NV, FULL, false><<<grid, THREADS, 0, s>>>(a);
+}
+
 template <int DT>
 void rows_dt(const LossArgs& a, hipStream_t s)
 {
     const dim3 grid(static_cast<unsigned>(a.x.rows));
+    // A row has nvec or (its head taken off) nvec - 1 whole vectors: past THREADS * FULL, every
+    // lane has FULL of them.
+    const int nvec = a.x.vocab / Fmt<DT>::E;
+    if (a.g.dx != nullptr && nvec >= 2) {
+        if (nvec <= 64 * 4) return held<DT, 64, 4, 0>(a, s);
+        if (nvec <= 64 * 8) return held<DT, 64, 8, 4>(a, s);
+        if (nvec <= 256 * 4) return held<DT, 256, 4, 2>(a, s);
+        if (nvec <= 256 * 8) return held<DT, 256, 8, 4>(a, s);
+        if (nvec <= 1024 * 4) return held<DT, 1024, 4, 2>(a, s);
+        if (nvec <= 1024 * 6) return held<DT, 1024, 6, 4>(a, s);
+        if (nvec <= 1024 * 8) return held<DT, 1024, 8, 6>(a, s);
+        if (nvec <= 1024 * 10) return held<DT, 1024, 10, 8>(a, s);
+        if (nvec <= 1024 * 12) return held<DT, 1024, 12, 10>(a, s);
+        if (nvec <= 1024 * 14) return held<DT, 1024, 14, 12>(a, s);
+        if (nvec <= 1024 * 16) return held<DT, 1024, 16, 14>(a, s);
+    }
     if (a.kind == kDistill)
         k_rows<DT, kRowThreads, true><<<grid, kRowThreads, 12u * a.k, s>>>(a);
     else
