@@ -18,6 +18,7 @@ struct LogitsView {
     int64_t stride;       // elements
     int32_t rows;
     int32_t vocab;
+    int32_t stream;       // set by the launch: read past the infinity cache
     float k_hi, k_lo;     // log2(e) / T as a sum of two positive floats, k_hi the larger
     double inv_t;         // 1 / T
 };
@@ -34,6 +35,7 @@ struct GradView {
 struct LossArgs {
     LogitsView x;
     GradView g;
+    void* workspace;              // MP_LOSS_WORKSPACE_BYTES, or NULL
     int32_t kind;
     int32_t k;                    // teacher's entries per row
     const int64_t* targets;       // NULL for distillation

@@ -55,26 +55,26 @@ __device__ __forceinline__ float widen(typename Fmt<DT>::T h)
     else return widen16<DT>(h);
 }
 
-#ifndef MPK_LOSS_NT_LOADS
-#define MPK_LOSS_NT_LOADS 1
-#endif
-#ifndef MPK_LOSS_NT_STORES
-#define MPK_LOSS_NT_STORES 1
-#endif
-// LAST: nothing reads these logits again in this call.
-template <int DT, bool LAST>
+// Logits that exceed the infinity cache are read past it (NT); smaller ones are
+// left where the layer before has just put them and a second pass will look for
+// them: LogitsView::stream says which.  Measured, cross-entropy bf16, logits in the
+// cache: 2048 x 50304 67 us against 80 with NT loads, 1024 x 50304 37 against 44;
+// not in the cache, 4096 x 50304 152 us with NT against 156, statistics of
+// 8192 x 128256 318 against 357.
+template <int DT, bool NT>
 __device__ __forceinline__ u32x4 load_vec(const typename Fmt<DT>::T* p)
 {
     const MPK_GLOBAL typename Fmt<DT>::Vec* q = (const MPK_GLOBAL typename Fmt<DT>::Vec*)(p);
-    return LAST && MPK_LOSS_NT_LOADS ? __builtin_nontemporal_load(q) : *q;
+    return NT ? __builtin_nontemporal_load(q) : *q;
 }
 
+// The gradient is read by another kernel, later, and stored past the caches: 3-10%
+// faster than plain stores at every size but the smallest, where they are equal.
 template <int DT>
 __device__ __forceinline__ void store_vec(typename Fmt<DT>::T* p, u32x4 v)
 {
     MPK_GLOBAL typename Fmt<DT>::Vec* q = (MPK_GLOBAL typename Fmt<DT>::Vec*)(p);
-    if (MPK_LOSS_NT_STORES) __builtin_nontemporal_store(v, q);
-    else *q = v;
+    __builtin_nontemporal_store(v, q);
 }
 
 template <int DT>
@@ -276,21 +276,25 @@ __device__ __forceinline__ Stat join(const Acc& a, const TeacherAcc& t, float k_
     return r;
 }
 
-// Sum of one double per lane, valid in all lanes.
-template <int THREADS>
-__device__ __forceinline__ double block_sum(double v)
+// Sums of N doubles per lane, valid in all lanes.
+template <int THREADS, int N>
+__device__ __forceinline__ void block_sum(double (&v)[N])
 {
     constexpr int W = THREADS / kWave;
-    __shared__ double part[W];
+    __shared__ double part[W][N];
 #pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) v += __shfl_xor(v, d);
-    __syncthreads();                     // the last use of part[] is over
-    if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = v;
+    for (int i = 0; i < N; ++i) {
+#pragma unroll
+        for (int d = 1; d < kWave; d <<= 1) v[i] += __shfl_xor(v[i], d);
+        if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave][i] = v[i];
+    }
     __syncthreads();
-    v = 0.0;
 #pragma unroll
-    for (int i = 0; i < W; ++i) v += part[i];
-    return v;
+    for (int i = 0; i < N; ++i) {
+        v[i] = 0.0;
+#pragma unroll
+        for (int j = 0; j < W; ++j) v[i] += part[j][i];
+    }
 }
 
 // ln s for s > 0 with an absolute error of about 4e-8 + 1e-8: s = 2^e f with f
@@ -473,15 +477,19 @@ struct TeacherRow {
     }
 };
 
+__device__ __forceinline__ void off_outputs(const LossArgs& a, int64_t row)
+{
+    if (threadIdx.x != 0) return;
+    if (a.loss != nullptr) a.loss[row] = 0.0f;
+    if (a.logp != nullptr) a.logp[row] = 0.0f;
+    if (a.lse != nullptr) a.lse[row] = 0.0f;
+    if (a.kl != nullptr) a.kl[row] = 0.0f;
+}
+
 template <int DT, int THREADS>
 __device__ __forceinline__ void off_row(const LossArgs& a, int64_t row, typename Fmt<DT>::T* dx)
 {
-    if (threadIdx.x == 0) {
-        if (a.loss != nullptr) a.loss[row] = 0.0f;
-        if (a.logp != nullptr) a.logp[row] = 0.0f;
-        if (a.lse != nullptr) a.lse[row] = 0.0f;
-        if (a.kl != nullptr) a.kl[row] = 0.0f;
-    }
+    off_outputs(a, row);
     if (dx != nullptr) zero_row<DT, THREADS>(dx, a.x.vocab);
 }
 
@@ -494,11 +502,12 @@ struct RowGrad {
     int off;
 };
 
-// The row's loss from its statistics: the outputs are written and the gradient's
-// numbers broadcast.  Only the first wave holds st; all lanes return the same.
+// The row's loss from its statistics: the outputs are written (`writes`) and the
+// gradient's numbers broadcast.  Only the first wave holds st; all lanes return
+// the same.
 template <int THREADS, bool DISTILL>
 __device__ __forceinline__ RowGrad row_formula(const LossArgs& a, int64_t row, const Stat& st, double w,
-                                               int64_t target, float xt)
+                                               int64_t target, float xt, bool writes = true)
 {
     __shared__ RowGrad out;
     if (threadIdx.x < kWave) {
@@ -519,14 +528,14 @@ __device__ __forceinline__ RowGrad row_formula(const LossArgs& a, int64_t row, c
             const double mass = a.teacher_lse != nullptr ? st.ts * one : 1.0;
             r.off = st.ts == 0.0 || mass == 0.0;
             const double loss = st.tc * one * a.x.inv_t + mass * (lse - norm);
-            if (threadIdx.x == 0) a.loss[row] = static_cast<float>(w * loss);
+            if (writes && threadIdx.x == 0) a.loss[row] = static_cast<float>(w * loss);
             mult = factor * w * mass;
             if (!(st.ts >= 0.0)) mult = __builtin_nan("");
             r.tm = st.tm;
             r.share = static_cast<float>(factor * w * one);
         } else {
             const double lp = (static_cast<double>(xt) - static_cast<double>(st.m)) * a.x.inv_t - ln_s;
-            mult = -factor * target_loss(a, row, w, lp, lse, threadIdx.x == 0);
+            mult = -factor * target_loss(a, row, w, lp, lse, writes && threadIdx.x == 0);
             if (target >= a.x.vocab) mult = __builtin_nan("");
             r.fix = static_cast<float>(mult * expm1_of(lp));
         }
@@ -564,7 +573,7 @@ __device__ __forceinline__ void store_shares(const TeacherRow<DT, THREADS>& t, t
 }
 
 // The statistics of whole vectors [from, nvec) of a row, 4 requested at a time.
-template <int DT, int THREADS, bool LAST>
+template <int DT, int THREADS, bool NT>
 __device__ __forceinline__ void stream_stats(Acc& acc, const typename Fmt<DT>::T* body, int from, int nvec,
                                              float k_hi, float k_lo)
 {
@@ -573,7 +582,7 @@ __device__ __forceinline__ void stream_stats(Acc& acc, const typename Fmt<DT>::T
     for (; i < nvec - (U - 1) * THREADS; i += U * THREADS) {
         u32x4 v[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) v[u] = load_vec<DT, LAST>(body + int64_t(i + u * THREADS) * E);
+        for (int u = 0; u < U; ++u) v[u] = load_vec<DT, NT>(body + int64_t(i + u * THREADS) * E);
 #pragma unroll
         for (int u = 0; u < U; u += 2) {
             float f[2][E];
@@ -584,13 +593,13 @@ __device__ __forceinline__ void stream_stats(Acc& acc, const typename Fmt<DT>::T
     }
     for (; i < nvec; i += THREADS) {
         float f[E];
-        unpack<DT>(load_vec<DT, LAST>(body + int64_t(i) * E), f);
+        unpack<DT>(load_vec<DT, NT>(body + int64_t(i) * E), f);
         add(acc, f, k_hi, k_lo);
     }
 }
 
 // The dense gradient of whole vectors [from, nvec) of a row.
-template <int DT, int THREADS>
+template <int DT, int THREADS, bool NT>
 __device__ __forceinline__ void stream_grad(const RowGrad& r, const typename Fmt<DT>::T* body,
                                             typename Fmt<DT>::T* dbody, int from, int nvec, float k_hi,
                                             float k_lo)
@@ -607,11 +616,11 @@ __device__ __forceinline__ void stream_grad(const RowGrad& r, const typename Fmt
     for (; i < nvec - (U - 1) * THREADS; i += U * THREADS) {
         u32x4 v[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) v[u] = load_vec<DT, true>(body + int64_t(i + u * THREADS) * E);
+        for (int u = 0; u < U; ++u) v[u] = load_vec<DT, NT>(body + int64_t(i + u * THREADS) * E);
 #pragma unroll
         for (int u = 0; u < U; ++u) one(v[u], i + u * THREADS);
     }
-    for (; i < nvec; i += THREADS) one(load_vec<DT, true>(body + int64_t(i) * E), i);
+    for (; i < nvec; i += THREADS) one(load_vec<DT, NT>(body + int64_t(i) * E), i);
 }
 
 // The statistics alone, one row per workgroup.
@@ -635,8 +644,8 @@ __global__ __launch_bounds__(THREADS) void k_rows_stats(LossArgs a)
         const float f[1] = {widen<DT>(x[one])};
         add(acc, f, a.x.k_hi, a.x.k_lo);
     }
-    // a gradient pass may follow (mp_token_logprob_grad): the logits stay in the caches
-    stream_stats<DT, THREADS, false>(acc, x + sp.head, 0, sp.nvec, a.x.k_hi, a.x.k_lo);
+    if (a.x.stream) stream_stats<DT, THREADS, true>(acc, x + sp.head, 0, sp.nvec, a.x.k_hi, a.x.k_lo);
+    else stream_stats<DT, THREADS, false>(acc, x + sp.head, 0, sp.nvec, a.x.k_hi, a.x.k_lo);
     TeacherAcc tacc;
     if constexpr (DISTILL) {
         for (int e = threadIdx.x; e < t.padded(a.k); e += THREADS) {
@@ -676,10 +685,16 @@ __global__ __launch_bounds__(THREADS) void k_rows_held(LossArgs a)
     if constexpr (DISTILL) entry = t.take(tid);
     // lanes past the end take the last vector once more, and drop it when it is used
     u32x4 v[NV > 0 ? NV : 1];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
+    auto at = [&](int i) {
         const int e = i * THREADS + tid;
-        v[i] = load_vec<DT, true>(x + sp.head + (i < FULL ? e : min(e, sp.nvec - 1)) * E);
+        return x + sp.head + (i < FULL ? e : min(e, sp.nvec - 1)) * E;
+    };
+    if (a.x.stream) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[i] = load_vec<DT, true>(at(i));
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[i] = load_vec<DT, false>(at(i));
     }
     const int one = sp.single(tid);
     const float single = one >= 0 ? widen<DT>(x[one]) : -__builtin_inff();
@@ -723,7 +738,7 @@ __global__ __launch_bounds__(THREADS) void k_rows_held(LossArgs a)
     const RowGrad r = row_formula<THREADS, DISTILL>(a, row, st, w, target, xt);
     if (DISTILL && r.off) return off_row<DT, THREADS>(a, row, dx);
     if constexpr (REST)
-        stream_grad<DT, THREADS>(r, x + sp.head, dx + sp.head, NV * THREADS, sp.nvec, k_hi, k_lo);
+        stream_grad<DT, THREADS, true>(r, x + sp.head, dx + sp.head, NV * THREADS, sp.nvec, k_hi, k_lo);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         float f[E];
@@ -739,6 +754,174 @@ __global__ __launch_bounds__(THREADS) void k_rows_held(LossArgs a)
     } else {
         __syncthreads();                // the dense gradient is stored
         if (tid == 0 && target < n) store_one<DT>(dx + target, r.fix);
+    }
+}
+
+// Few rows, less than the chip has room for: a row is cut into parts of kPartVecs
+// vectors, one workgroup each.  The first launch leaves every part's (m, s) in
+// the workspace -- part 0 also takes what is read singly: the ends of the row,
+// the target's logit, the teacher's sums, all before any gradient is stored.  In
+// the second every workgroup joins its row's parts and stores its part of the
+// gradient; part 0 writes the outputs.
+constexpr int kPartThreads = 256;
+constexpr int kPartHeld = 4;                              // vectors a lane
+constexpr int kPartVecs = kPartThreads * kPartHeld;
+constexpr int kMaxParts = kWave;                          // joined by one wave
+
+struct PartSum {
+    double s;
+    float m;
+    float unused;
+};
+
+struct PartRow {
+    double ts, tc;
+    float tm, xt;
+    double unused;
+};
+
+// Workspace of a split launch: rows * parts PartSum, then rows PartRow.
+struct Parts {
+    PartSum* sum;
+    PartRow* row;
+    int parts, vecs;       // per row; vectors of a part
+};
+
+template <int DT, bool DISTILL>
+__global__ __launch_bounds__(kPartThreads) void k_part_stats(LossArgs a, Parts w)
+{
+    using T = typename Fmt<DT>::T;
+    extern __shared__ __align__(16) char lds[];
+    const int64_t row = blockIdx.x / static_cast<unsigned>(w.parts);
+    const int part = static_cast<int>(blockIdx.x % static_cast<unsigned>(w.parts));
+    const int n = a.x.vocab;
+    const T* x = static_cast<const T*>(a.x.x) + row * a.x.stride;
+    const int64_t target = DISTILL ? 0 : read_table(a.targets + row);
+    if (target < 0 || (a.weights != nullptr && read_table(a.weights + row) == 0.0f)) return;
+    const void* align = a.g.dx != nullptr ? static_cast<const T*>(a.g.dx) + row * a.g.stride : x;
+    const Span<DT> sp(align, n);
+    Acc acc;
+    TeacherAcc tacc;
+    float xt = 0.0f;
+    if (part == 0) {
+        const int one = sp.single(threadIdx.x);
+        if (one >= 0) {
+            const float f[1] = {widen<DT>(x[one])};
+            add(acc, f, a.x.k_hi, a.x.k_lo);
+        }
+        if constexpr (DISTILL) {
+            const TeacherRow<DT, kPartThreads> t(a, row, x, lds);
+            for (int e = threadIdx.x; e < a.k; e += kPartThreads) {
+                auto entry = t.take(e);
+                t.look_up(entry);
+                t.put(tacc, entry, e);
+            }
+        } else {
+            xt = target < n ? widen<DT>(x[target]) : __builtin_nanf("");
+        }
+    }
+    const int lo = part * w.vecs;
+    stream_stats<DT, kPartThreads, false>(acc, x + sp.head, lo, min(lo + w.vecs, sp.nvec), a.x.k_hi,
+                                          a.x.k_lo);
+    const Stat st = join<kPartThreads, DISTILL>(acc, tacc, a.x.k_hi, a.x.k_lo);
+    if (threadIdx.x == 0) {
+        w.sum[row * w.parts + part] = PartSum{st.s, st.m, 0.0f};
+        if (part == 0) w.row[row] = PartRow{st.ts, st.tc, st.tm, xt, 0.0};
+    }
+}
+
+template <int DT, bool DISTILL>
+__global__ __launch_bounds__(kPartThreads) void k_part_grad(LossArgs a, Parts w)
+{
+    using T = typename Fmt<DT>::T;
+    constexpr int E = Fmt<DT>::E;
+    extern __shared__ __align__(16) char lds[];
+    // without a gradient: one workgroup a row, for the outputs
+    const unsigned blocks = a.g.dx != nullptr ? w.parts : 1;
+    const int64_t row = blockIdx.x / blocks;
+    const int part = static_cast<int>(blockIdx.x % blocks);
+    const int tid = threadIdx.x;
+    const int n = a.x.vocab;
+    const T* x = static_cast<const T*>(a.x.x) + row * a.x.stride;
+    T* dx = a.g.dx != nullptr ? static_cast<T*>(a.g.dx) + row * a.g.stride : nullptr;
+    const int64_t target = DISTILL ? 0 : read_table(a.targets + row);
+    const double weight = a.weights != nullptr ? static_cast<double>(read_table(a.weights + row)) : 1.0;
+    const float k_hi = a.x.k_hi, k_lo = a.x.k_lo;
+    const Span<DT> sp(dx, n);
+    const int lo = part * w.vecs, hi = min(lo + w.vecs, sp.nvec);
+    const int one = part == 0 ? sp.single(tid) : -1;
+    auto zero = [&] {
+        if (part == 0) off_outputs(a, row);
+        if (dx == nullptr) return;
+        const u32x4 z = {0u, 0u, 0u, 0u};
+        for (int i = lo + tid; i < hi; i += kPartThreads) store_vec<DT>(dx + sp.head + int64_t(i) * E, z);
+        if (one >= 0) store_one<DT>(dx + one, 0.0f);
+    };
+    if (target < 0 || weight == 0.0) return zero();
+
+    u32x4 v[kPartHeld];
+    float single = 0.0f;
+    if (dx != nullptr) {
+#pragma unroll
+        for (int i = 0; i < kPartHeld; ++i)
+            v[i] = load_vec<DT, false>(x + sp.head + int64_t(max(min(lo + i * kPartThreads + tid, hi - 1), 0)) * E);
+        if (one >= 0) single = widen<DT>(x[one]);
+    }
+    const TeacherRow<DT, kPartThreads> t(a, row, x, lds);
+    if constexpr (DISTILL) {
+        if (dx != nullptr) {
+            TeacherAcc unused;
+            for (int e = tid; e < t.padded(a.k); e += kPartThreads) {
+                auto entry = t.take(e);
+                // the ids that lie in this part: nobody else stores there
+                const int64_t at = entry.id - sp.head;
+                const bool ends = at < 0 || at >= int64_t(sp.nvec) * E;
+                const bool mine = ends ? part == 0 : at >= int64_t(lo) * E && at < int64_t(hi) * E;
+                if (!mine || entry.id >= n) entry.id = -1;
+                t.look_up(entry);
+                t.put(unused, entry, e);
+            }
+        }
+    }
+    Stat st{-FLT_MAX, 0.0, 0.0f, 0.0, 0.0};
+    float xt = 0.0f;
+    if (tid < kWave) {
+        double sum[1] = {0.0};
+        if (tid < w.parts) {
+            const PartSum p = w.sum[row * w.parts + tid];
+            st.m = p.m;
+            sum[0] = p.s;
+        }
+        join_lanes<kWave>(st.m, sum, k_hi, k_lo);
+        st.s = sum[0];
+        const PartRow r = w.row[row];
+        st.tm = r.tm;
+        st.ts = r.ts;
+        st.tc = r.tc;
+        xt = r.xt;
+    }
+    const RowGrad r = row_formula<kPartThreads, DISTILL>(a, row, st, weight, target, xt, part == 0);
+    if (DISTILL && r.off) return zero();
+    if (dx == nullptr) return;
+#pragma unroll
+    for (int i = 0; i < kPartHeld; ++i) {
+        float f[E];
+        unpack<DT>(v[i], f);
+#pragma unroll
+        for (int j = 0; j < E; ++j) f[j] = share_of<DT>(f[j], r.m, k_hi, k_lo) * r.c;
+        const int at = lo + i * kPartThreads + tid;
+        if (at < hi) store_vec<DT>(dx + sp.head + int64_t(at) * E, pack<DT>(f));
+    }
+    stream_grad<DT, kPartThreads, false>(r, x + sp.head, dx + sp.head, lo + kPartVecs, hi, k_hi, k_lo);
+    if (one >= 0) store_one<DT>(dx + one, share_of<DT>(single, r.m, k_hi, k_lo) * r.c);
+    if constexpr (DISTILL) {
+        store_shares<DT, kPartThreads>(t, dx, r);
+    } else {
+        const int64_t at = target - sp.head;
+        const bool ends = at < 0 || at >= int64_t(sp.nvec) * E;
+        const bool mine = ends ? part == 0 : at >= int64_t(lo) * E && at < int64_t(hi) * E;
+        __syncthreads();                // this part of the dense gradient is stored
+        if (mine && tid == 0 && target < n) store_one<DT>(dx + target, r.fix);
     }
 }
 
@@ -796,12 +979,19 @@ __global__ __launch_bounds__(kGradThreads) void k_logprob_grad(LogitsView v, Gra
         if (mine) xt = widen<DT>(x[te]);
     }
     float single = one >= 0 ? widen<DT>(x[one]) : 0.0f;
-    for (int i = lo + tid; i < hi; i += kGradThreads) {
+    auto vec = [&](u32x4 raw, int i) {
         float f[E];
-        unpack<DT>(load_vec<DT, true>(x + sp.head + int64_t(i) * E), f);
+        unpack<DT>(raw, f);
 #pragma unroll
         for (int j = 0; j < E; ++j) f[j] = q(f[j]) * c;
         store_vec<DT>(dx + sp.head + int64_t(i) * E, pack<DT>(f));
+    };
+    if (v.stream) {
+        for (int i = lo + tid; i < hi; i += kGradThreads)
+            vec(load_vec<DT, true>(x + sp.head + int64_t(i) * E), i);
+    } else {
+        for (int i = lo + tid; i < hi; i += kGradThreads)
+            vec(load_vec<DT, false>(x + sp.head + int64_t(i) * E), i);
     }
     if (one >= 0) store_one<DT>(dx + one, q(single) * c);
     if (mine) {
@@ -830,25 +1020,26 @@ __global__ __launch_bounds__(kPairThreads) void k_pairs(PairArgs a)
         for (int64_t r = last + tid; r < a.rows; r += kPairThreads) a.dlogp[r] = 0.0f;
         return;
     }
-    double pi[2], per[2];
+    // sums of lp and counts of targets of the chosen and the rejected sequence, reduced together
+    double v[4] = {0.0, 0.0, 0.0, 0.0};
     int64_t begin[2], end[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int64_t seq = pair + i * pairs;
         begin[i] = clamp_row(read_table(a.seq_start + seq), a.rows);
         end[i] = clamp_row(read_table(a.seq_start + seq + 1), a.rows);
-        double sum = 0.0, live = 0.0;
+#pragma unroll 4
         for (int64_t r = begin[i] + tid; r < end[i]; r += kPairThreads) {
-            sum += static_cast<double>(a.logp[r]);
-            live += a.targets[r] >= 0 ? 1.0 : 0.0;
+            v[2 * i] += static_cast<double>(a.logp[r]);
+            v[2 * i + 1] += a.targets[r] >= 0 ? 1.0 : 0.0;
         }
-        sum = block_sum<kPairThreads>(sum);
-        per[i] = 1.0;
-        if (a.length_mean) {
-            live = block_sum<kPairThreads>(live);
-            per[i] = live > 0.0 ? 1.0 / live : 0.0;
-        }
-        pi[i] = sum * per[i];
+    }
+    block_sum<kPairThreads>(v);
+    double pi[2], per[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        per[i] = !a.length_mean ? 1.0 : v[2 * i + 1] > 0.0 ? 1.0 / v[2 * i + 1] : 0.0;
+        pi[i] = v[2 * i] * per[i];
     }
     double ref[2] = {0.0, 0.0};
     if (a.ref_logp != nullptr) {
@@ -891,10 +1082,20 @@ __global__ __launch_bounds__(kCountThreads) void k_target_count(int64_t n, const
 {
     __shared__ int64_t part[kCountThreads / kWave];
     int64_t c = 0;
-#pragma unroll 8
-    for (int64_t i = threadIdx.x; i < n; i += kCountThreads) c += targets[i] >= 0 ? 1 : 0;
+    // a ballot per wave and 64 targets, 8 requested at a time; lanes past n take the last one again
+    for (int64_t from = 0; from < n; from += 8 * kCountThreads) {
+        int64_t t[8];
 #pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) c += __shfl_xor(c, d);
+        for (int u = 0; u < 8; ++u) {
+            const int64_t i = from + u * kCountThreads + threadIdx.x;
+            t[u] = targets[i < n ? i : n - 1];
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const bool in = from + u * kCountThreads + threadIdx.x < n;
+            c += __builtin_popcountll(__builtin_amdgcn_ballot_w64(in && t[u] >= 0));
+        }
+    }
     if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = c;
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -930,13 +1131,63 @@ void stats(const LossArgs& a, hipStream_t s)
         k_rows_stats<DT, THREADS, false><<<grid, THREADS, 0, s>>>(a);
 }
 
+// Split the rows over several workgroups?  Fills `w` in the workspace if so.
+// A whole row takes a workgroup's own time (cross-entropy with gradient, bf16:
+// 8.6 us for 20000 logits, 11.5 for 50304, 18.9 for 128256, up to about 100 rows
+// alike); its parts take 10 us however long the row and grow with the rows, being
+// read twice.  Split against whole: 128256 logits, 1 row 10.1 us against 18.9, 61
+// rows 15.1 against 20.7, 100 rows 18.7 against 21.3, 160 rows 24.8 against 22.4;
+// 50304 logits, 1 row 10.0 against 11.6, 100 rows 13.6 against 13.6; 20000 logits,
+// 1 row 9.6 against 8.1; 32001 fp32 logits, 61 rows 12.0 against 11.1.
+constexpr int kSplitRows = 100;
+constexpr int kSplitVocab = 48 * 1024;
+
 template <int DT>
-void rows_dt(const LossArgs& a, hipStream_t s)
+bool split(const LossArgs& a, Parts* w)
 {
+    const int nvec = a.x.vocab / Fmt<DT>::E;
+    if (a.workspace == nullptr || a.x.rows > kSplitRows || a.x.vocab < kSplitVocab) return false;
+    int vecs = kPartVecs;
+    while ((nvec + vecs - 1) / vecs > kMaxParts) vecs += kPartVecs;
+    w->vecs = vecs;
+    w->parts = (nvec + vecs - 1) / vecs;
+    const size_t sums = sizeof(PartSum) * a.x.rows * w->parts;
+    if (sums + sizeof(PartRow) * a.x.rows > MP_LOSS_WORKSPACE_BYTES) return false;
+    w->sum = static_cast<PartSum*>(a.workspace);
+    w->row = reinterpret_cast<PartRow*>(static_cast<char*>(a.workspace) + sums);
+    return true;
+}
+
+constexpr int64_t kCacheBytes = int64_t(256) << 20;      // the infinity cache of an MI355X
+
+template <int DT>
+int64_t logits_bytes(const LogitsView& x)
+{
+    return int64_t(x.rows) * x.vocab * static_cast<int64_t>(sizeof(typename Fmt<DT>::T));
+}
+
+template <int DT>
+void rows_dt(LossArgs a, hipStream_t s)
+{
+    a.x.stream = logits_bytes<DT>(a.x) > kCacheBytes;
+    Parts w;
+    if (split<DT>(a, &w)) {
+        const unsigned rows = static_cast<unsigned>(a.x.rows);
+        const dim3 all(rows * w.parts), grid(a.g.dx != nullptr ? rows * w.parts : rows);
+        if (a.kind == kDistill) {
+            k_part_stats<DT, true><<<all, kPartThreads, teacher_lds(a), s>>>(a, w);
+            k_part_grad<DT, true><<<grid, kPartThreads, teacher_lds(a), s>>>(a, w);
+        } else {
+            k_part_stats<DT, false><<<all, kPartThreads, 0, s>>>(a, w);
+            k_part_grad<DT, false><<<grid, kPartThreads, 0, s>>>(a, w);
+        }
+        return;
+    }
     // A row has nvec or (its head taken off) nvec - 1 whole vectors: past THREADS * FULL, every
     // lane has FULL of them.  Below 2 there may be none.
     const int nvec = a.x.vocab / Fmt<DT>::E;
-    if (a.g.dx == nullptr) return nvec <= 64 * 8 ? stats<DT, 64>(a, s) : stats<DT, 256>(a, s);
+    if (a.g.dx == nullptr)
+        return nvec <= 64 * 8 ? stats<DT, 64>(a, s) : stats<DT, 256>(a, s);
     if (nvec < 2) return held<DT, 64, 0, 0, true>(a, s);
     if (nvec <= 64 * 4) return held<DT, 64, 4, 0>(a, s);
     if (nvec <= 64 * 8) return held<DT, 64, 8, 4>(a, s);
@@ -967,9 +1218,14 @@ void rows_dt(const LossArgs& a, hipStream_t s)
 }
 
 template <int DT>
-void grad_dt(const LogitsView& x, const int64_t* targets, const float* lse, const float* dlogp,
+void grad_dt(LogitsView x, const int64_t* targets, const float* lse, const float* dlogp,
              const GradView& g, hipStream_t s)
 {
+    // Here the pass before has read the logits, and read all of them: past half the cache little of
+    // them is left.  Statistics and gradient of 2048 x 50304 bf16 (206 MB): 102 us with NT loads
+    // against 116 where they came from memory, 118 against 113 where they started in the cache;
+    // 1024 x 50304: 64 against 62, and 63 against 61.
+    x.stream = logits_bytes<DT>(x) > kCacheBytes / 2;
     // chunks of at least 8 vectors a lane; few enough that the launch stays in range
     const int nvec = x.vocab / Fmt<DT>::E + 1;
     int per = 8 * kGradThreads;

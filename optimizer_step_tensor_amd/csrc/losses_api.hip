@@ -148,6 +148,7 @@ mp_status run_rows(const mp_logits* x, const mp_logits_grad* g, LossArgs& a, mp_
     if (st != MP_OK) return st;
     a.x = view_of(x);
     a.g = view_of(x, g);
+    a.workspace = x->workspace;
     hipError_t e = mpk::launch_rows(a, x->dtype, static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return set_error(MP_ERR_HIP, "loss launch: %s", hipGetErrorString(e));
     return set_ok();
@@ -295,6 +296,7 @@ mp_status mp_preference_loss(const mp_logits* x, const int64_t* targets, int64_t
     LossArgs a{};
     a.kind = mpk::kLogprob;
     a.x = view_of(x);
+    a.workspace = x->workspace;
     a.targets = targets;
     a.logp = logp;
     a.lse = lse;
