@@ -25,6 +25,7 @@ constexpr int kBF16 = MP_BF16, kFP16 = MP_FP16, kFP32 = MP_FP32;
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
@@ -549,24 +550,28 @@ __device__ __forceinline__ RowGrad row_formula(const LossArgs& a, int64_t row, c
 
 // The elements that differ from the dense gradient, after all of it is stored:
 // the target's, or each teacher's id's, q_id mass - sum of the shares of that id.
-// An id that comes twice is stored twice, the same value.  k comparisons per
-// entry: for k <= 256 a small part of the row's time.
+// An id that comes twice is stored twice, the same value.  Every entry is compared
+// with all k, four at a time.
 template <int DT, int THREADS>
 __device__ __forceinline__ void store_shares(const TeacherRow<DT, THREADS>& t, typename Fmt<DT>::T* dx,
                                              const RowGrad& r)
 {
     const int k = t.a.k;
     const float k_hi = t.a.x.k_hi, k_lo = t.a.x.k_lo;
+    // the values become shares; each lane its own entries
+    for (int e = threadIdx.x; e < t.padded(k); e += THREADS)
+        t.v[e] = t.id[e] >= 0 ? exp2_hw(scaled(t.v[e], r.tm, k_hi, k_lo)) : 0.0f;
     __syncthreads();
     for (int e = threadIdx.x; e < k; e += THREADS) {
         const int id = t.id[e];
         if (id < 0) continue;
         float p = 0.0f;
+#pragma unroll 4
         for (int i = 0; i < k; i += 4) {
             const i32x4 four = *reinterpret_cast<const i32x4*>(t.id + i);
+            const f32x4 share = *reinterpret_cast<const f32x4*>(t.v + i);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (four[j] == id) p += exp2_hw(scaled(t.v[i + j], r.tm, k_hi, k_lo));
+            for (int j = 0; j < 4; ++j) p += four[j] == id ? share[j] : 0.0f;
         }
         store_one<DT>(dx + id, share_of<DT>(t.xs[e], r.m, k_hi, k_lo) * r.c - r.share * p);
     }
@@ -1133,20 +1138,22 @@ void stats(const LossArgs& a, hipStream_t s)
 
 // Split the rows over several workgroups?  Fills `w` in the workspace if so.
 // A whole row takes a workgroup's own time (cross-entropy with gradient, bf16:
-// 8.6 us for 20000 logits, 11.5 for 50304, 18.9 for 128256, up to about 100 rows
+// 8.1 us for 20000 logits, 11.8 for 50304, 19.3 for 128256, up to about 100 rows
 // alike); its parts take 10 us however long the row and grow with the rows, being
-// read twice.  Split against whole: 128256 logits, 1 row 10.1 us against 18.9, 61
-// rows 15.1 against 20.7, 100 rows 18.7 against 21.3, 160 rows 24.8 against 22.4;
-// 50304 logits, 1 row 10.0 against 11.6, 100 rows 13.6 against 13.6; 20000 logits,
-// 1 row 9.6 against 8.1; 32001 fp32 logits, 61 rows 12.0 against 11.1.
-constexpr int kSplitRows = 100;
+// read twice.  Split against whole: 128256 logits, 1 row 10.7 us against 19.3, 61
+// rows 15.1 against 20.7, 100 rows 19.3 against 21.5, 192 rows 31.4 against 25.1;
+// 50304 logits, 1 row 10.4 against 11.8, 100 rows 13.8 against 13.4; 20000 logits,
+// 1 row 9.6 against 8.1; 60000 fp32 logits, 1 row 10.2 against 12.3, 32 rows 12.5
+// against 13.1, 100 rows 17.8 against 15.2.
+template <int DT>
+constexpr int kSplitRows = Fmt<DT>::E == 8 ? 100 : 40;
 constexpr int kSplitVocab = 48 * 1024;
 
 template <int DT>
 bool split(const LossArgs& a, Parts* w)
 {
     const int nvec = a.x.vocab / Fmt<DT>::E;
-    if (a.workspace == nullptr || a.x.rows > kSplitRows || a.x.vocab < kSplitVocab) return false;
+    if (a.workspace == nullptr || a.x.rows > kSplitRows<DT> || a.x.vocab < kSplitVocab) return false;
     int vecs = kPartVecs;
     while ((nvec + vecs - 1) / vecs > kMaxParts) vecs += kPartVecs;
     w->vecs = vecs;
@@ -1187,8 +1194,12 @@ void rows_dt(LossArgs a, hipStream_t s)
     // lane has FULL of them.  Below 2 there may be none.
     const int nvec = a.x.vocab / Fmt<DT>::E;
     if (a.g.dx == nullptr)
-        return nvec <= 64 * 8 ? stats<DT, 64>(a, s) : stats<DT, 256>(a, s);
+        return nvec <= 64 * 8 && (a.kind != kDistill || a.k <= 64) ? stats<DT, 64>(a, s)
+                                                                   : stats<DT, 256>(a, s);
     if (nvec < 2) return held<DT, 64, 0, 0, true>(a, s);
+    // a wave a row, unless a teacher's list needs more lanes: 30 rows of 3551 with 201 entries
+    // 40 us with one wave, 8 us with four
+    if (a.kind == kDistill && a.k > 64 && nvec <= 256 * 4) return held<DT, 256, 4, 0>(a, s);
     if (nvec <= 64 * 4) return held<DT, 64, 4, 0>(a, s);
     if (nvec <= 64 * 8) return held<DT, 64, 8, 4>(a, s);
     if (nvec <= 256 * 4) return held<DT, 256, 4, 2>(a, s);
