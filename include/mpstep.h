@@ -566,7 +566,10 @@ mp_status mp_token_logprob(const mp_logits* x, const int64_t* targets, float* lo
 /* The gradient of sum_r dlogp[r] * lp_r for any dlogp, from the lse of
  * mp_token_logprob on the same logits:
  *   dx_rj = scale/T * dlogp[r] * ((j = t) - q_rj).
- * A row with dlogp[r] == 0 is written as zeros without being read. */
+ * A row with dlogp[r] == 0 is written as zeros without being read.  q is as
+ * exact as lse is in fp32: where |lse| is 1000, to 3e-5; an lse beyond 2e38 (a
+ * row of nothing but the type's lowest value) gives a gradient that is not
+ * finite.  The fused calls below have no such limit. */
 mp_status mp_token_logprob_grad(const mp_logits* x, const int64_t* targets, const float* lse,
                                 const float* dlogp, const mp_logits_grad* grad, mp_stream stream);
 

@@ -498,12 +498,13 @@ def _matrix(x, name):
 
 def logits(x, temperature=1.0, workspace=None):
     """The mp_logits of a 2-D tensor [rows, vocab] (rows may be strided).  workspace: a tensor of
-    MP_LOSS_WORKSPACE_BYTES uint8 on its GPU, used where there are few rows.  The struct holds
-    addresses: keep the tensors alive while work that uses them is enqueued."""
+    MP_LOSS_WORKSPACE_BYTES uint8 on its GPU, used where there are few rows.  The struct keeps
+    the tensors it describes."""
     data, rows, vocab, stride = _matrix(x, "logits")
     w = _array(workspace, torch.uint8, MP_LOSS_WORKSPACE_BYTES, "workspace", x.device)
     out = Logits(data, rows, vocab, stride, _LOGITS_DTYPE[x.dtype], temperature, w)
     out.torch = (x.dtype, x.device, rows, vocab)
+    out.keep = (x, workspace)
     return out
 
 
@@ -515,6 +516,7 @@ def logits_grad(dx, scale=1.0, dev_scale=None, dev_count=None):
     out = LogitsGrad(data, stride, _array(dev_scale, torch.float32, 1, "dev_scale", dx.device),
                      _array(dev_count, torch.int64, 1, "dev_count", dx.device), scale)
     out.torch = (dx.dtype, dx.device, rows, vocab)
+    out.keep = (dx, dev_scale, dev_count)
     return out
 
 
@@ -540,6 +542,7 @@ def teacher(values, ids, lse=None):
                   _array(lse, torch.float32, rows, "teacher lse", values.device), k,
                   _LOGITS_DTYPE[values.dtype])
     out.torch = (values.device, rows)
+    out.keep = (values, ids, lse)
     return out
 
 

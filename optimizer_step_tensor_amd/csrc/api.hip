@@ -417,7 +417,11 @@ mp_status set_error(mp_status st, const char* fmt, ...)
     va_start(ap, fmt);
     vsnprintf(buf, sizeof buf, fmt, ap);
     va_end(ap);
-    return fail(st, "%s", buf);
+    try {
+        return fail(st, "%s", buf);
+    } catch (const std::bad_alloc&) {
+        return st;             // without its detail
+    }
 }
 
 mp_status set_ok()

@@ -216,7 +216,9 @@ struct Stat {
     double ts, tc;
 };
 
-// (m, s[]) joined over groups of WIDTH lanes.
+// (m, s[]) joined over groups of WIDTH lanes.  An infinite sum (a share of the
+// teacher's where the student has none) that is scaled to nothing is nothing; NaN
+// stays.
 template <int WIDTH, int N>
 __device__ __forceinline__ void join_lanes(float& m, double (&s)[N], float k_hi, float k_lo)
 {
@@ -226,7 +228,7 @@ __device__ __forceinline__ void join_lanes(float& m, double (&s)[N], float k_hi,
     const double scale = static_cast<double>(exp2_hw(scaled(own, m, k_hi, k_lo)));
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        s[i] *= scale;
+        s[i] = scale == 0.0 && __builtin_isinf(s[i]) ? 0.0 : s[i] * scale;
 #pragma unroll
         for (int d = 1; d < WIDTH; d <<= 1) s[i] += __shfl_xor(s[i], d);
     }
@@ -473,7 +475,7 @@ struct TeacherRow {
         const float p = exp2_hw(scaled(r.v, m, a.x.k_hi, a.x.k_lo));
         acc.m = m;
         acc.s = acc.s * old + p;
-        acc.c *= old;
+        acc.c = old != 0.0f ? acc.c * old : 0.0f;
         if (p != 0.0f) acc.c += p * (r.v - r.x);      // a share of 0 adds 0 whatever the student has
     }
 };

@@ -228,6 +228,55 @@ def test_many_rows(mp, kind, rows):
     run_all(mp, kind, 4200, min(rows, 300), 0.7, LAYOUTS[0], rows, False)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("V", [49151, 49152, 50305, 66001, 131079, 1050003])
+def test_few_long_rows_split_over_workgroups(mp, kind, V):
+    """Rows cut into parts in the workspace: every layout; parts that end inside the row's last
+    vectors; more vectors than the parts hold at once (past 2^20 logits)."""
+    i = KINDS.index(kind)
+    for layout in LAYOUTS if V < 1000000 else LAYOUTS[2:]:
+        run_all(mp, kind, V, 1 + i, [1.0, 0.7, 2.0][i], layout, 300 + i, True)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_both_sides_of_the_split(mp, kind):
+    rows = 101 if kind != "fp32" else 41
+    for n in (rows - 1, rows):
+        x, t = make_x(gen(16, n), n, 49300, kind)
+        t[::5] = -1
+        bx, bd, lx, lg, factor, keep = state_for(mp, x, kind, ws=workspace(mp))
+        loss = empty(n)
+        mp.mp_cross_entropy(lx, dev(t), None, loss, lg)
+        r = ref.cross_entropy(x, t, 1.0, None, factor, kind)
+        check((n, "loss"), loss, r["loss"], r["tol_loss"])
+        check((n, "dx"), bd.t, r["dx"], r["tol_dx"])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("V,k", [(40, 7), (9000, 300), (60000, 70)])
+def test_student_masked_where_the_teacher_is_not(mp, kind, V, k):
+    """An id with a share but a student's logit of -inf: an infinite loss (whatever the order the
+    entries are joined in), a finite gradient; with a share of 0 there, a finite loss."""
+    import torch
+    rng = gen(17, V)
+    x, t = make_x(rng, 4, V, kind)
+    ids = np.stack([rng.choice(V, min(k, V), replace=False) for _ in range(4)])
+    vals = f32(rng.normal(0, 1, ids.shape))
+    x[0, ids[0, 0]] = -np.inf
+    x[1, ids[1, -1]] = -np.inf
+    x[2, ids[2, 1]] = -np.inf
+    vals[0, 0], vals[1, -1] = 1.0, -60.0
+    vals[2, 1] = -np.inf
+    for ws in (None, workspace(mp)):
+        bx, bd, lx, lg, factor, keep = state_for(mp, x, kind, ws=ws)
+        loss = empty(4)
+        mp.mp_distill_loss(lx, mp.teacher(dev(vals), dev(ids)), None, loss, lg)
+        r = ref.distill(x, vals, ids, None, 1.0, None, factor, kind)
+        check((kind, V, "loss"), loss, r["loss"], r["tol_loss"])
+        check((kind, V, "dx"), bd.t, r["dx"], r["tol_dx"])
+        assert bool(torch.isinf(loss[:2]).all()) and bool(torch.isfinite(loss[2:]).all())
+
+
 def test_more_rows_than_a_16_bit_grid(mp):
     """70001 rows of 24 logits; every tenth switched off."""
     import torch
