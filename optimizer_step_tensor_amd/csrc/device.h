@@ -1,5 +1,6 @@
 // Device code shared by the update step's kernels (kernels.hip) and the losses'
-// (losses.hip): the 16-bit formats, address spaces and table reads.
+// (losses.hip): the 16-bit formats, address spaces, table
+// reads and the renumbering of workgroups over the XCDs.
 #pragma once
 
 #include "internal.h"
@@ -81,6 +82,20 @@ __device__ __forceinline__ T read_table(const T* p)
         for (int i = 0; i < int(sizeof(T) / 8); ++i) x.w[i] = q[i];
         return __builtin_bit_cast(T, x);
     }
+}
+
+// The chunk block b of a G-block grid starts at.  Workgroup b runs on XCD
+// b mod 8; this renumbering gives each XCD SPAN consecutive chunks per turn of
+// 8 * SPAN blocks.  It permutes 0..G-1: blocks of the last, incomplete turn
+// keep their own number.
+template <int SPAN = MPK_XCD_SPAN>
+__device__ __forceinline__ int64_t xcd_first_chunk(int64_t b, int64_t G)
+{
+    constexpr int64_t span = SPAN;
+    constexpr int64_t turn = span * kXcds;
+    if (span <= 1 || b >= (G / turn) * turn) return b;
+    const int64_t t = b / turn, within = b % turn;
+    return t * turn + (within % kXcds) * span + within / kXcds;
 }
 
 }  // namespace

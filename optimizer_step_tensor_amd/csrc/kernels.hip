@@ -106,20 +106,6 @@ __device__ __forceinline__ void store_h4(uint16_t* p, const H4& r, int nv)
     }
 }
 
-// The chunk block b of a G-block grid starts at.  Workgroup b runs on XCD
-// b mod 8; this renumbering gives each XCD SPAN consecutive chunks per turn of
-// 8 * SPAN blocks.  It permutes 0..G-1: blocks of the last, incomplete turn
-// keep their own number.
-template <int SPAN = MPK_XCD_SPAN>
-__device__ __forceinline__ int64_t xcd_first_chunk(int64_t b, int64_t G)
-{
-    constexpr int64_t span = SPAN;
-    constexpr int64_t turn = span * kXcds;
-    if (span <= 1 || b >= (G / turn) * turn) return b;
-    const int64_t t = b / turn, within = b % turn;
-    return t * turn + (within % kXcds) * span + within / kXcds;
-}
-
 // Run pass(full, base) over a chunk of `len` elements: every complete
 // 2048-element block pass with full = true_type (no bounds checks at all),
 // then the one partial pass, if any, with full = false_type.
