@@ -3,7 +3,9 @@
 // accumulated, the last folded in), then unscale/norm, AdamW and the scaler in
 // one call.  Step 2: token weights computed on the device from device counts,
 // and both micro-batches folded into the norm and AdamW passes as one resident
-// group.  The inputs are chosen so that the results have closed forms, which
+// group.  A last part starts from logits: their cross-entropy's gradient, scaled
+// by the state's own S and divided by a device count, is a micro-batch's
+// gradient.  The inputs are chosen so that the results have closed forms, which
 // the program checks; it prints one line and exits 0 on success.
 //
 // Gradients are 2^-10 everywhere in both micro-batches, so with token counts
@@ -179,6 +181,57 @@ int main()
     (void)hipFree(d_counts);
     (void)hipFree(d_weights);
 
+    // From logits.  Equal logits over 256 ids: every loss is ln 256, and the gradient of the mean
+    // over the 16 rows with a target is 2^-12 everywhere and -255 * 2^-12 at the targets, all
+    // exact in bf16; the 4 rows without a target are zeros.  As the only micro-batch of a plan
+    // whose one tensor the logits are, its sum of squares is 16 * 255 * 256 * 2^-24.
+    const int64_t rows = 20, vocab = 256, cells = rows * vocab;
+    std::vector<int64_t> targets(rows);
+    for (int64_t r = 0; r < rows; ++r) targets[r] = r % 5 == 4 ? -100 : 7 * r;
+    void *x = nullptr, *dx = nullptr, *p32[3] = {nullptr, nullptr, nullptr}, *p16 = nullptr;
+    int64_t *d_targets = nullptr, *d_n = nullptr;
+    float* d_loss = nullptr;
+    HIP_OK(hipMalloc(&x, cells * 2));
+    HIP_OK(hipMalloc(&dx, cells * 2));
+    HIP_OK(hipMalloc(&p16, cells * 2));
+    for (void*& q : p32) {
+        HIP_OK(hipMalloc(&q, cells * 4));
+        HIP_OK(hipMemset(q, 0, cells * 4));
+    }
+    HIP_OK(hipMalloc(&d_targets, rows * sizeof(int64_t)));
+    HIP_OK(hipMalloc(&d_n, sizeof(int64_t)));
+    HIP_OK(hipMalloc(&d_loss, rows * sizeof(float)));
+    HIP_OK(hipMemset(x, 0, cells * 2));
+    HIP_OK(hipMemcpy(d_targets, targets.data(), rows * sizeof(int64_t), hipMemcpyHostToDevice));
+    mp_plan* plan2 = nullptr;
+    mp_gradset* set3 = nullptr;
+    mp_state* state2 = nullptr;
+    MP_OK_(mp_plan_create(1, &cells, MP_BF16, nullptr, &p32[0], &p32[1], &p32[2], &p16, nullptr,
+                          &plan2));
+    MP_OK_(mp_gradset_create(plan2, &dx, &set3));
+    MP_OK_(mp_state_create(&cfg, &state2));
+    const float* d_scale = nullptr;
+    MP_OK_(mp_state_scale_ptr(state2, &d_scale));
+    const mp_logits lx = {x, rows, vocab, vocab, MP_BF16, 1.0f, nullptr};
+    const mp_logits_grad lg = {dx, vocab, d_scale, d_n, 1.0f};
+    MP_OK_(mp_target_count(rows, d_targets, d_n, stream));
+    MP_OK_(mp_cross_entropy(&lx, d_targets, nullptr, d_loss, &lg, stream));
+    MP_OK_(mp_update_step(plan2, state2, set3, 1.0f, 1, 0.0f, &hp, stream));
+    mp_stats stats4;
+    std::vector<float> loss(rows);
+    MP_OK_(mp_state_read(state2, &stats4, stream));
+    HIP_OK(hipMemcpyAsync(loss.data(), d_loss, rows * sizeof(float), hipMemcpyDeviceToHost, stream));
+    HIP_OK(hipStreamSynchronize(stream));
+    if (stats4.found_inf != 0 || stats4.sumsq != 16.0 * 255.0 * 256.0 * std::ldexp(1.0, -24)) ++bad;
+    for (int64_t r = 0; r < rows; ++r)
+        if (loss[r] != (targets[r] < 0 ? 0.0f : static_cast<float>(std::log(256.0)))) ++bad;
+    mp_gradset_destroy(set3);
+    mp_state_destroy(state2);
+    mp_plan_destroy(plan2);
+    for (void* q : {x, dx, p32[0], p32[1], p32[2], p16, static_cast<void*>(d_targets),
+                    static_cast<void*>(d_n), static_cast<void*>(d_loss)})
+        (void)hipFree(q);
+
     mp_gradset_destroy(set1);
     mp_gradset_destroy(set2);
     mp_state_destroy(state);
@@ -189,8 +242,9 @@ int main()
     (void)hipStreamDestroy(stream);
 
     std::printf("c_api_step: %s  params %lld  sumsq %.17g (want %.17g)  norm %.9g  "
-                "max |w - closed form| %.3g after step 1, %.3g after step 2, %.3g after step 3\n",
+                "max |w - closed form| %.3g after step 1, %.3g after step 2, %.3g after step 3, "
+                "sumsq from logits %.17g\n",
                 bad ? "MISMATCH" : "ok", static_cast<long long>(total), stats.sumsq, want_sumsq,
-                static_cast<double>(stats.grad_norm), worst, worst2, worst3);
+                static_cast<double>(stats.grad_norm), worst, worst2, worst3, stats4.sumsq);
     return bad ? 1 : 0;
 }
