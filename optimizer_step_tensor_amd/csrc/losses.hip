@@ -14,11 +14,23 @@
 // against about 15 VALU operations.
 #include <float.h>
 
-#include "device.h"
+#include "internal.h"
 #include "losses.h"
 
 namespace mpk {
 namespace {
+
+// Global pointers become global_load/global_store, not flat instructions; a
+// uniform address that nothing writes while the kernel runs (targets, per-row
+// inputs, the loss scale, a count) is one scalar load.
+#define MPK_GLOBAL __attribute__((address_space(1)))
+#define MPK_CONST __attribute__((address_space(4)))
+
+template <class T>
+__device__ __forceinline__ T read_table(const T* p)
+{
+    return *(const MPK_CONST T*)(p);
+}
 
 constexpr int kBF16 = MP_BF16, kFP16 = MP_FP16, kFP32 = MP_FP32;
 
@@ -53,7 +65,8 @@ template <int DT>
 __device__ __forceinline__ float widen(typename Fmt<DT>::T h)
 {
     if constexpr (DT == kFP32) return h;
-    else return widen16<DT>(h);
+    else if constexpr (DT == kBF16) return __uint_as_float(static_cast<uint32_t>(h) << 16);
+    else return static_cast<float>(__builtin_bit_cast(_Float16, h));
 }
 
 // Logits that exceed the infinity cache are read past it (NT); smaller ones are
@@ -129,7 +142,8 @@ __device__ __forceinline__ void store_one(typename Fmt<DT>::T* p, float f)
 {
     MPK_GLOBAL typename Fmt<DT>::T* q = (MPK_GLOBAL typename Fmt<DT>::T*)(p);
     if constexpr (DT == kFP32) *q = f;
-    else *q = static_cast<uint16_t>(round16<DT>(f));
+    else if constexpr (DT == kBF16) *q = __builtin_bit_cast(uint16_t, static_cast<__bf16>(f));
+    else *q = __builtin_bit_cast(uint16_t, static_cast<_Float16>(f));
 }
 
 // How n elements are dealt to lanes: `head` single ones up to the first 16-byte
@@ -421,7 +435,7 @@ __device__ __forceinline__ float teacher_value(const LossArgs& a, int64_t i)
     h += wide ? 2 * i : i;
     const uint32_t lo = h[0], hi = h[wide ? 1 : 0];
     const float f = __uint_as_float(hi << 16 | (wide ? lo : 0u));      // fp32 and bf16
-    return a.teacher_dtype == kFP16 ? widen16<kFP16>(lo) : f;
+    return a.teacher_dtype == kFP16 ? widen<kFP16>(static_cast<uint16_t>(lo)) : f;
 }
 
 // The teacher's side of one row.  Every lane takes entries tid, tid + THREADS, ..: the first is
@@ -937,6 +951,17 @@ __global__ __launch_bounds__(kPartThreads) void k_part_grad(LossArgs a, Parts w)
 // fma, whose result is small where q matters; the second only counts for fp32
 // results (a 16-bit result is rounded at 2^-9 or 2^-12).
 constexpr int kGradThreads = 256;
+constexpr int kGradSpan = 64;       // consecutive chunks an XCD takes
+
+// Workgroup b of G runs on XCD b mod 8: this renumbering gives each XCD runs of
+// kGradSpan consecutive chunks (the last, incomplete turn keeps its numbers).
+__device__ __forceinline__ unsigned xcd_chunk(unsigned b, unsigned G)
+{
+    constexpr unsigned turn = kGradSpan * kXcds;
+    if (b >= G / turn * turn) return b;
+    const unsigned t = b / turn, within = b % turn;
+    return t * turn + within % kXcds * kGradSpan + within / kXcds;
+}
 
 template <int DT>
 __global__ __launch_bounds__(kGradThreads) void k_logprob_grad(LogitsView v, GradView g,
@@ -946,7 +971,7 @@ __global__ __launch_bounds__(kGradThreads) void k_logprob_grad(LogitsView v, Gra
 {
     using T = typename Fmt<DT>::T;
     constexpr int E = Fmt<DT>::E;
-    const unsigned block = static_cast<unsigned>(xcd_first_chunk<>(blockIdx.x, gridDim.x));
+    const unsigned block = xcd_chunk(blockIdx.x, gridDim.x);
     const int64_t row = block / static_cast<unsigned>(chunks);
     const int chunk = static_cast<int>(block % static_cast<unsigned>(chunks));
     const int tid = threadIdx.x;
