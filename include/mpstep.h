@@ -510,9 +510,10 @@ mp_status mp_adamw_step_fp8(mp_plan* plan, mp_state* state, const mp_gradset* la
  *    in a fixed order (the same bits on every run); losses are formed in
  *    binary64 and rounded once; a gradient is formed in fp32 and rounded once
  *    (round to nearest even) to the logits' type.
- *  - rows = 0 is allowed and enqueues nothing.
- *  - The logits must be memory of the current device (else MP_ERR_INVALID).
- *    Nothing is allocated; the calls may be captured into a graph.
+ *  - rows = 0 is allowed and enqueues nothing (but the pairs of a preference loss).
+ *  - The logits (the count, of mp_target_count) and the stream must belong to
+ *    the current device (else MP_ERR_INVALID).  Nothing is allocated; the calls
+ *    may be captured into a graph.
  * ------------------------------------------------------------------------ */
 
 /* fp32 logits; the 16-bit formats are MP_BF16 and MP_FP16.  Not a format of a plan. */

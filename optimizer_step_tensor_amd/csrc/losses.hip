@@ -1266,7 +1266,7 @@ void grad_dt(LogitsView x, const int64_t* targets, const float* lse, const float
     // 1024 x 50304: 64 against 62, and 63 against 61.
     x.stream = logits_bytes<DT>(x) > kCacheBytes / 2;
     // Chunks of 2 vectors a lane, runs of 64 of them on an XCD: what is in flight is then one
-    // compact piece of memory (pass over 3088 x 128256 bf16 with a third of the rows off: 207 us,
+    // compact piece of memory (pass over 3087 x 128256 bf16 with a third of the rows off: 207 us,
     // 6.5 TB/s; 8 vectors 246 us; without the runs 216 us).  More where the launch would get too large.
     const int nvec = x.vocab / Fmt<DT>::E + 1;
     int per = 2 * kGradThreads;

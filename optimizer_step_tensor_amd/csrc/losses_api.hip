@@ -89,9 +89,9 @@ mp_status check_array(const void* p, uintptr_t align, int64_t rows, bool require
     return MP_OK;
 }
 
-// The work is launched on the current device: the logits have to live there,
-// and the stream, too.
-mp_status check_place(const void* data, mp_stream stream)
+// The work is launched on the current device: `data` (the logits) has to live
+// there, and the stream, too.
+mp_status check_place(const void* data, const char* what, mp_stream stream)
 {
     int cur = -1, dev = -1;
     hipError_t e = hipGetDevice(&cur);
@@ -100,10 +100,10 @@ mp_status check_place(const void* data, mp_stream stream)
     e = hipPointerGetAttributes(&at, data);
     if (e != hipSuccess) (void)hipGetLastError();        // an address that HIP does not know
     if (e != hipSuccess || (at.type != hipMemoryTypeDevice && at.type != hipMemoryTypeManaged))
-        return set_error(MP_ERR_INVALID, "the logits are not device memory");
+        return set_error(MP_ERR_INVALID, "%s: not device memory", what);
     if (at.device != cur)
-        return set_error(MP_ERR_INVALID, "the logits are on device %d but device %d is current",
-                         at.device, cur);
+        return set_error(MP_ERR_INVALID, "%s: on device %d but device %d is current", what, at.device,
+                         cur);
     if (stream != nullptr) {
         e = hipStreamGetDevice(static_cast<hipStream_t>(stream), &dev);
         if (e != hipSuccess) return set_error(MP_ERR_HIP, "hipStreamGetDevice: %s", hipGetErrorString(e));
@@ -144,7 +144,7 @@ GradView view_of(const mp_logits* x, const mp_logits_grad* g)
 mp_status run_rows(const mp_logits* x, const mp_logits_grad* g, LossArgs& a, mp_stream stream)
 {
     if (x->rows == 0) return set_ok();
-    mp_status st = check_place(x->data, stream);
+    mp_status st = check_place(x->data, "logits", stream);
     if (st != MP_OK) return st;
     a.x = view_of(x);
     a.g = view_of(x, g);
@@ -163,6 +163,7 @@ mp_status mp_target_count(int64_t n, const int64_t* targets, int64_t* count, mp_
     if (n < 0) return set_error(MP_ERR_INVALID, "n must be >= 0");
     mp_status st = check_array(targets, 8, n, true, "targets");
     if (st == MP_OK) st = check_array(count, 8, 1, true, "count");
+    if (st == MP_OK) st = check_place(count, "count", stream);
     if (st != MP_OK) return st;
     hipError_t e = mpk::launch_target_count(n, targets, count, static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return set_error(MP_ERR_HIP, "target count launch: %s", hipGetErrorString(e));
@@ -196,7 +197,7 @@ mp_status mp_token_logprob_grad(const mp_logits* x, const int64_t* targets, cons
     if (st == MP_OK) st = check_array(dlogp, 4, x->rows, true, "dlogp");
     if (st != MP_OK) return st;
     if (x->rows == 0) return set_ok();
-    st = check_place(x->data, stream);
+    st = check_place(x->data, "logits", stream);
     if (st != MP_OK) return st;
     hipError_t e = mpk::launch_logprob_grad(view_of(x), targets, lse, dlogp, view_of(x, grad), x->dtype,
                                             static_cast<hipStream_t>(stream));
@@ -290,7 +291,8 @@ mp_status mp_preference_loss(const mp_logits* x, const int64_t* targets, int64_t
     if (st == MP_OK) st = check_array(logp, 4, x->rows, true, "logp");
     if (st == MP_OK) st = check_array(lse, 4, x->rows, true, "lse");
     if (st == MP_OK) st = check_array(dlogp, 4, x->rows, true, "dlogp");
-    if (st == MP_OK) st = check_place(x->rows > 0 ? x->data : seq_start, stream);
+    if (st == MP_OK) st = check_place(x->rows > 0 ? x->data : seq_start,
+                                      x->rows > 0 ? "logits" : "seq_start", stream);
     if (st != MP_OK) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
     LossArgs a{};

@@ -238,6 +238,26 @@ def test_few_long_rows_split_over_workgroups(mp, kind, V):
         run_all(mp, kind, V, 1 + i, [1.0, 0.7, 2.0][i], layout, 300 + i, True)
 
 
+@pytest.mark.parametrize("with_ws", [False, True])
+def test_a_row_of_16_million_logits(mp, with_ws):
+    rng = gen(18)
+    x, t = make_x(rng, 1, (1 << 24) + 5, "bf16")
+    ws = workspace(mp) if with_ws else None
+    bx, bd, lx, lg, factor, keep = state_for(mp, x, "bf16", pad=1, shift=1, dpad=1, dshift=1, ws=ws)
+    loss = empty(1)
+    mp.mp_cross_entropy(lx, dev(t), None, loss, lg)
+    r = ref.cross_entropy(x, t, 1.0, None, factor, "bf16")
+    check("loss", loss, r["loss"], r["tol_loss"])
+    check("dx", bd.t, r["dx"], r["tol_dx"])
+    assert bx.untouched() and bd.untouched()
+    lp, lse = empty(1), empty(1)
+    mp.mp_token_logprob(lx, dev(t), lp, lse)
+    r = ref.logprob(x, t, 1.0, np.array([-0.5]), factor, "bf16")
+    mp.mp_token_logprob_grad(lx, dev(t), lse, dev([-0.5]), lg)
+    for k, v in (("logp", lp), ("lse", lse), ("dx", bd.t)):
+        check(k, v, r[k], r["tol_" + k])
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_both_sides_of_the_split(mp, kind):
     rows = 101 if kind != "fp32" else 41
@@ -696,6 +716,10 @@ def test_logits_that_are_not_device_memory_are_refused(mp):
         lp = empty(4)
         with pytest.raises(mp.MpError):
             mp.mp_preference_loss(lx, t, 1, t, None, mp.preference_cfg(), loss, loss, lp, lp, lp)
+        n = torch.zeros(1, dtype=torch.int64, pin_memory=pinned)
+        with pytest.raises(mp.MpError):
+            mp.mp_target_count(t, n.data_ptr())
+        assert int(n) == 0
     torch.cuda.synchronize()
     assert bool((loss == -55.0).all())
 
