@@ -230,6 +230,60 @@ struct Stat {
     double ts, tc;
 };
 
+// A lane's value and its partner's D lanes away, for reductions whose earlier steps
+// have made groups of D lanes alike: within 16 lanes by DPP (the mirrors then
+// stand for an exchange of 4 and of 8), beyond by gfx950's row swaps, which give
+// both values to all lanes.  A reduction of a wave is some 10 cycles a step this
+// way; through the LDS crossbar (ds_bpermute) a step waits over 100.
+template <int D>
+__device__ __forceinline__ void across(uint32_t v, uint32_t& a, uint32_t& b)
+{
+    if constexpr (D == 32) {
+        const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        a = r[0];
+        b = r[1];
+    } else if constexpr (D == 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        a = r[0];
+        b = r[1];
+    } else {
+        constexpr int ctrl = D == 1   ? 0xB1      // quad_perm [1, 0, 3, 2]
+                             : D == 2 ? 0x4E      // quad_perm [2, 3, 0, 1]
+                             : D == 4 ? 0x141     // row_half_mirror
+                                      : 0x140;    // row_mirror
+        a = v;
+        b = static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), ctrl, 0xF, 0xF, true));
+    }
+}
+
+// Maximum and sum over groups of WIDTH lanes, in all of them.  (The order of the
+// two operands differs between lanes, the result does not.)
+template <int WIDTH, int D = 1>
+__device__ __forceinline__ float lanes_max(float v)
+{
+    if constexpr (D < WIDTH) {
+        uint32_t a, b;
+        across<D>(__float_as_uint(v), a, b);
+        return lanes_max<WIDTH, 2 * D>(__builtin_fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    }
+    return v;
+}
+
+template <int WIDTH, int D = 1>
+__device__ __forceinline__ double lanes_sum(double v)
+{
+    if constexpr (D < WIDTH) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, v);
+        uint32_t a0, b0, a1, b1;
+        across<D>(static_cast<uint32_t>(u), a0, b0);
+        across<D>(static_cast<uint32_t>(u >> 32), a1, b1);
+        const double a = __builtin_bit_cast(double, uint64_t(a1) << 32 | a0);
+        const double b = __builtin_bit_cast(double, uint64_t(b1) << 32 | b0);
+        return lanes_sum<WIDTH, 2 * D>(a + b);
+    }
+    return v;
+}
+
 // (m, s[]) joined over groups of WIDTH lanes.  An infinite sum (a share of the
 // teacher's where the student has none) that is scaled to nothing is nothing; NaN
 // stays.
@@ -237,14 +291,11 @@ template <int WIDTH, int N>
 __device__ __forceinline__ void join_lanes(float& m, double (&s)[N], float k_hi, float k_lo)
 {
     const float own = m;
-#pragma unroll
-    for (int d = 1; d < WIDTH; d <<= 1) m = __builtin_fmaxf(m, __shfl_xor(m, d));
+    m = lanes_max<WIDTH>(m);
     const double scale = static_cast<double>(exp2_hw(scaled(own, m, k_hi, k_lo)));
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        s[i] = scale == 0.0 && __builtin_isinf(s[i]) ? 0.0 : s[i] * scale;
-#pragma unroll
-        for (int d = 1; d < WIDTH; d <<= 1) s[i] += __shfl_xor(s[i], d);
+        s[i] = lanes_sum<WIDTH>(scale == 0.0 && __builtin_isinf(s[i]) ? 0.0 : s[i] * scale);
     }
 }
 
@@ -301,8 +352,7 @@ __device__ __forceinline__ void block_sum(double (&v)[N])
     __shared__ double part[W][N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-#pragma unroll
-        for (int d = 1; d < kWave; d <<= 1) v[i] += __shfl_xor(v[i], d);
+        v[i] = lanes_sum<kWave>(v[i]);
         if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave][i] = v[i];
     }
     __syncthreads();
@@ -370,18 +420,49 @@ __device__ __forceinline__ double expm1_of(double d)
     return d > -0.5 ? d + k3_of(d) : exp_of(d) - 1.0;
 }
 
+// What a row's formula takes besides the logits: requested when the row is, so
+// that the first wave does not wait for it between the statistics and the gradient.
+struct RowIn {
+    int64_t target;
+    double w;
+    double factor;              // of the gradient
+    float advantage, old_logp, ref_logp, teacher_lse;
+    // no target, or no weight: nothing of the row is used
+    __device__ __forceinline__ bool off() const { return target < 0 || w == 0.0; }
+};
+
+template <bool DISTILL>
+__device__ __forceinline__ RowIn row_in(const LossArgs& a, int64_t row)
+{
+    RowIn r{};
+    r.w = a.weights != nullptr ? static_cast<double>(read_table(a.weights + row)) : 1.0;
+    if constexpr (DISTILL) {
+        if (a.teacher_lse != nullptr) r.teacher_lse = read_table(a.teacher_lse + row);
+    } else {
+        r.target = read_table(a.targets + row);
+        if (a.kind == kPolicy) {
+            r.advantage = read_table(a.advantage + row);
+            r.old_logp = read_table(a.old_logp + row);
+            if (a.ref_logp != nullptr) r.ref_logp = read_table(a.ref_logp + row);
+        }
+    }
+    if (a.g.dx != nullptr) r.factor = grad_factor(a.g);
+    return r;
+}
+
 // The row's loss from lp; writes the per-row outputs (lane 0) and returns
 // dL/dlp.
-__device__ __forceinline__ double target_loss(const LossArgs& a, int64_t row, double w, double lp,
+__device__ __forceinline__ double target_loss(const LossArgs& a, int64_t row, const RowIn& in, double lp,
                                               double lse, bool writes)
 {
+    const double w = in.w;
     double loss = 0.0, slope = 0.0, kl = 0.0;
     if (a.kind == kXent) {
         loss = -w * lp;
         slope = -w;
     } else if (a.kind == kPolicy) {
-        const double adv = static_cast<double>(read_table(a.advantage + row));
-        const double rho = exp_of(lp - static_cast<double>(read_table(a.old_logp + row)));
+        const double adv = static_cast<double>(in.advantage);
+        const double rho = exp_of(lp - static_cast<double>(in.old_logp));
         const double lo = 1.0 - static_cast<double>(a.clip_low);
         const double hi = 1.0 + static_cast<double>(a.clip_high);
         if (adv != 0.0) {
@@ -393,7 +474,7 @@ __device__ __forceinline__ double target_loss(const LossArgs& a, int64_t row, do
             loss = slope = lp;
         }
         if (a.ref_logp != nullptr) {
-            const double d = static_cast<double>(read_table(a.ref_logp + row)) - lp;
+            const double d = static_cast<double>(in.ref_logp) - lp;
             kl = k3_of(d);
             const double c = static_cast<double>(a.kl_coef);
             if (c != 0.0) {
@@ -523,14 +604,14 @@ struct RowGrad {
 // gradient's numbers broadcast.  Only the first wave holds st; all lanes return
 // the same.
 template <int THREADS, bool DISTILL>
-__device__ __forceinline__ RowGrad row_formula(const LossArgs& a, int64_t row, const Stat& st, double w,
-                                               int64_t target, float xt, bool writes = true)
+__device__ __forceinline__ RowGrad row_formula(const LossArgs& a, int64_t row, const RowIn& in,
+                                               const Stat& st, float xt, bool writes = true)
 {
     __shared__ RowGrad out;
     if (threadIdx.x < kWave) {
         const double ln_s = log_sum(st.s);
         const double lse = static_cast<double>(st.m) * a.x.inv_t + ln_s;
-        const double factor = a.g.dx != nullptr ? grad_factor(a.g) : 0.0;
+        const double w = in.w, factor = in.factor;
         double mult;
         RowGrad r{};
         if constexpr (DISTILL) {
@@ -539,7 +620,7 @@ __device__ __forceinline__ RowGrad row_formula(const LossArgs& a, int64_t row, c
             const double top = static_cast<double>(st.tm) * a.x.inv_t;
             double norm = top + log_sum(st.ts), one = 1.0 / st.ts;
             if (a.teacher_lse != nullptr) {
-                norm = static_cast<double>(read_table(a.teacher_lse + row));
+                norm = static_cast<double>(in.teacher_lse);
                 one = exp_of(top - norm);
             }
             const double mass = a.teacher_lse != nullptr ? st.ts * one : 1.0;
@@ -552,8 +633,8 @@ __device__ __forceinline__ RowGrad row_formula(const LossArgs& a, int64_t row, c
             r.share = static_cast<float>(factor * w * one);
         } else {
             const double lp = (static_cast<double>(xt) - static_cast<double>(st.m)) * a.x.inv_t - ln_s;
-            mult = -factor * target_loss(a, row, w, lp, lse, writes && threadIdx.x == 0);
-            if (target >= a.x.vocab) mult = __builtin_nan("");
+            mult = -factor * target_loss(a, row, in, lp, lse, writes && threadIdx.x == 0);
+            if (in.target >= a.x.vocab) mult = __builtin_nan("");
             r.fix = static_cast<float>(mult * expm1_of(lp));
         }
         r.m = st.m;
@@ -653,9 +734,9 @@ __global__ __launch_bounds__(THREADS) void k_rows_stats(LossArgs a)
     const int64_t row = blockIdx.x;
     const int n = a.x.vocab;
     const T* x = static_cast<const T*>(a.x.x) + row * a.x.stride;
-    const int64_t target = DISTILL ? 0 : read_table(a.targets + row);
-    const double w = a.weights != nullptr ? static_cast<double>(read_table(a.weights + row)) : 1.0;
-    if (target < 0 || w == 0.0) return off_row<DT, THREADS>(a, row, nullptr);
+    const RowIn in = row_in<DISTILL>(a, row);
+    if (in.off()) return off_row<DT, THREADS>(a, row, nullptr);
+    const int64_t target = in.target;
     const TeacherRow<DT, THREADS> t(a, row, x, lds);
     const float xt = DISTILL ? 0.0f : target < n ? widen<DT>(x[target]) : __builtin_nanf("");
     const Span<DT> sp(x, n);
@@ -676,7 +757,7 @@ __global__ __launch_bounds__(THREADS) void k_rows_stats(LossArgs a)
         }
     }
     const Stat st = join<THREADS, DISTILL>(acc, tacc, a.x.k_hi, a.x.k_lo);
-    const RowGrad r = row_formula<THREADS, DISTILL>(a, row, st, w, target, xt);
+    const RowGrad r = row_formula<THREADS, DISTILL>(a, row, in, st, xt);
     if (DISTILL && r.off) off_row<DT, THREADS>(a, row, nullptr);
 }
 
@@ -695,9 +776,9 @@ __global__ __launch_bounds__(THREADS) void k_rows_held(LossArgs a)
     const int n = a.x.vocab;
     const T* x = static_cast<const T*>(a.x.x) + row * a.x.stride;
     T* dx = static_cast<T*>(a.g.dx) + row * a.g.stride;
-    const int64_t target = DISTILL ? 0 : read_table(a.targets + row);
-    const double w = a.weights != nullptr ? static_cast<double>(read_table(a.weights + row)) : 1.0;
-    if (target < 0 || w == 0.0) return off_row<DT, THREADS>(a, row, dx);
+    const RowIn in = row_in<DISTILL>(a, row);
+    if (in.off()) return off_row<DT, THREADS>(a, row, dx);
+    const int64_t target = in.target;
 
     const float k_hi = a.x.k_hi, k_lo = a.x.k_lo;
     const Span<DT> sp(dx, n);
@@ -756,7 +837,7 @@ __global__ __launch_bounds__(THREADS) void k_rows_held(LossArgs a)
         }
     }
     const Stat st = join<THREADS, DISTILL>(acc, tacc, k_hi, k_lo);
-    const RowGrad r = row_formula<THREADS, DISTILL>(a, row, st, w, target, xt);
+    const RowGrad r = row_formula<THREADS, DISTILL>(a, row, in, st, xt);
     if (DISTILL && r.off) return off_row<DT, THREADS>(a, row, dx);
     if constexpr (REST)
         stream_grad<DT, THREADS, true>(r, x + sp.head, dx + sp.head, NV * THREADS, sp.nvec, k_hi, k_lo);
@@ -865,8 +946,8 @@ __global__ __launch_bounds__(kPartThreads) void k_part_grad(LossArgs a, Parts w)
     const int n = a.x.vocab;
     const T* x = static_cast<const T*>(a.x.x) + row * a.x.stride;
     T* dx = a.g.dx != nullptr ? static_cast<T*>(a.g.dx) + row * a.g.stride : nullptr;
-    const int64_t target = DISTILL ? 0 : read_table(a.targets + row);
-    const double weight = a.weights != nullptr ? static_cast<double>(read_table(a.weights + row)) : 1.0;
+    const RowIn in = row_in<DISTILL>(a, row);
+    const int64_t target = in.target;
     const float k_hi = a.x.k_hi, k_lo = a.x.k_lo;
     const Span<DT> sp(dx, n);
     const int lo = part * w.vecs, hi = min(lo + w.vecs, sp.nvec);
@@ -878,7 +959,7 @@ __global__ __launch_bounds__(kPartThreads) void k_part_grad(LossArgs a, Parts w)
         for (int i = lo + tid; i < hi; i += kPartThreads) store_vec<DT>(dx + sp.head + int64_t(i) * E, z);
         if (one >= 0) store_one<DT>(dx + one, 0.0f);
     };
-    if (target < 0 || weight == 0.0) return zero();
+    if (in.off()) return zero();
 
     u32x4 v[kPartHeld];
     float single = 0.0f;
@@ -921,7 +1002,7 @@ __global__ __launch_bounds__(kPartThreads) void k_part_grad(LossArgs a, Parts w)
         st.tc = r.tc;
         xt = r.xt;
     }
-    const RowGrad r = row_formula<kPartThreads, DISTILL>(a, row, st, weight, target, xt, part == 0);
+    const RowGrad r = row_formula<kPartThreads, DISTILL>(a, row, in, st, xt, part == 0);
     if (DISTILL && r.off) return zero();
     if (dx == nullptr) return;
 #pragma unroll
