@@ -480,7 +480,7 @@ def _array(x, dtype, n, name, device=None):
         raise TypeError("%s must be a %s tensor, not %s" % (name, dtype, x.dtype))
     if x.numel() < n or not x.is_contiguous():
         raise ValueError("%s must be contiguous, with %d elements" % (name, n))
-    if not x.is_cuda or (device is not None and x.device != device):
+    if x.device != device if device is not None else not x.is_cuda:
         raise ValueError("%s must be on the logits' GPU" % name)
     return x.data_ptr()
 
@@ -558,76 +558,91 @@ def _grad_of(x, grad):
     return ctypes.byref(grad)
 
 
-def _rows_of(x):
-    """A checker of per-row arrays for the logits x."""
+def _place(x):
+    """rows and GPU of the logits x (None: made of addresses)."""
     have = getattr(x, "torch", None)
-    device = have[1] if have is not None else None
-    return lambda a, dtype, name, n=x.rows: _array(a, dtype, n, name, device)
+    return x.rows, have[1] if have is not None else None
+
+
+def _stream_of(stream, device):
+    """`stream`, or the current one of the logits' GPU."""
+    if stream is None and device is not None and _raw_stream is not None:
+        return _raw_stream(device.index)
+    return _stream(stream)
+
+
+_F32, _I64 = torch.float32, torch.int64
 
 
 def mp_target_count(targets, count, n=None, stream=None):
     """count[0] = how many targets (int64, the first n or all) are >= 0."""
     n = targets.numel() if n is None else int(n)
-    _check(lib().mp_target_count(n, _array(targets, torch.int64, n, "targets"),
-                                 _array(count, torch.int64, 1, "count"), _stream(stream)))
+    _check(lib().mp_target_count(n, _array(targets, _I64, n, "targets"),
+                                 _array(count, _I64, 1, "count"), _stream(stream)))
 
 
 def mp_token_logprob(x, targets, logp, lse=None, stream=None):
     """x: logits(...); targets: int64 [rows]; logp and lse: float32 [rows], written."""
-    f = _rows_of(x)
-    _check(lib().mp_token_logprob(ctypes.byref(x), f(targets, torch.int64, "targets"),
-                                  f(logp, torch.float32, "logp"), f(lse, torch.float32, "lse"),
-                                  _stream(stream)))
+    n, d = _place(x)
+    _check(lib().mp_token_logprob(ctypes.byref(x), _array(targets, _I64, n, "targets", d),
+                                  _array(logp, _F32, n, "logp", d),
+                                  _array(lse, _F32, n, "lse", d), _stream_of(stream, d)))
 
 
 def mp_token_logprob_grad(x, targets, lse, dlogp, grad, stream=None):
-    f = _rows_of(x)
-    _check(lib().mp_token_logprob_grad(ctypes.byref(x), f(targets, torch.int64, "targets"),
-                                       f(lse, torch.float32, "lse"),
-                                       f(dlogp, torch.float32, "dlogp"), _grad_of(x, grad),
-                                       _stream(stream)))
+    n, d = _place(x)
+    _check(lib().mp_token_logprob_grad(ctypes.byref(x), _array(targets, _I64, n, "targets", d),
+                                       _array(lse, _F32, n, "lse", d),
+                                       _array(dlogp, _F32, n, "dlogp", d), _grad_of(x, grad),
+                                       _stream_of(stream, d)))
 
 
 def mp_cross_entropy(x, targets, weights, loss, grad=None, stream=None):
-    f = _rows_of(x)
-    _check(lib().mp_cross_entropy(ctypes.byref(x), f(targets, torch.int64, "targets"),
-                                  f(weights, torch.float32, "weights"),
-                                  f(loss, torch.float32, "loss"), _grad_of(x, grad),
-                                  _stream(stream)))
+    n, d = _place(x)
+    _check(lib().mp_cross_entropy(ctypes.byref(x), _array(targets, _I64, n, "targets", d),
+                                  _array(weights, _F32, n, "weights", d),
+                                  _array(loss, _F32, n, "loss", d), _grad_of(x, grad),
+                                  _stream_of(stream, d)))
 
 
 def mp_policy_loss(x, targets, old_logp, ref_logp, advantage, weights, cfg, loss, logp=None,
                    kl=None, grad=None, stream=None):
-    f, t = _rows_of(x), torch.float32
-    _check(lib().mp_policy_loss(ctypes.byref(x), f(targets, torch.int64, "targets"),
-                                f(old_logp, t, "old_logp"), f(ref_logp, t, "ref_logp"),
-                                f(advantage, t, "advantage"), f(weights, t, "weights"),
-                                ctypes.byref(cfg), f(loss, t, "loss"), f(logp, t, "logp"),
-                                f(kl, t, "kl"), _grad_of(x, grad), _stream(stream)))
+    n, d = _place(x)
+    _check(lib().mp_policy_loss(ctypes.byref(x), _array(targets, _I64, n, "targets", d),
+                                _array(old_logp, _F32, n, "old_logp", d),
+                                _array(ref_logp, _F32, n, "ref_logp", d),
+                                _array(advantage, _F32, n, "advantage", d),
+                                _array(weights, _F32, n, "weights", d), ctypes.byref(cfg),
+                                _array(loss, _F32, n, "loss", d), _array(logp, _F32, n, "logp", d),
+                                _array(kl, _F32, n, "kl", d), _grad_of(x, grad),
+                                _stream_of(stream, d)))
 
 
 def mp_preference_loss(x, targets, n_pairs, seq_start, ref_logp, cfg, loss, seq_logp, logp, lse,
                        dlogp, grad=None, stream=None):
-    f, t, n = _rows_of(x), torch.float32, int(n_pairs)
-    _check(lib().mp_preference_loss(ctypes.byref(x), f(targets, torch.int64, "targets"), n,
-                                    f(seq_start, torch.int64, "seq_start", 2 * n + 1),
-                                    f(ref_logp, t, "ref_logp", 2 * n), ctypes.byref(cfg),
-                                    f(loss, t, "loss", n), f(seq_logp, t, "seq_logp", 2 * n),
-                                    f(logp, t, "logp"), f(lse, t, "lse"), f(dlogp, t, "dlogp"),
-                                    _grad_of(x, grad), _stream(stream)))
+    (n, d), p = _place(x), int(n_pairs)
+    _check(lib().mp_preference_loss(ctypes.byref(x), _array(targets, _I64, n, "targets", d), p,
+                                    _array(seq_start, _I64, 2 * p + 1, "seq_start", d),
+                                    _array(ref_logp, _F32, 2 * p, "ref_logp", d), ctypes.byref(cfg),
+                                    _array(loss, _F32, p, "loss", d),
+                                    _array(seq_logp, _F32, 2 * p, "seq_logp", d),
+                                    _array(logp, _F32, n, "logp", d), _array(lse, _F32, n, "lse", d),
+                                    _array(dlogp, _F32, n, "dlogp", d), _grad_of(x, grad),
+                                    _stream_of(stream, d)))
 
 
 def mp_distill_loss(x, teacher, weights, loss, grad=None, stream=None):
-    f = _rows_of(x)
-    if hasattr(teacher, "torch") and hasattr(x, "torch"):
-        if teacher.torch[0] != x.torch[1]:
+    n, d = _place(x)
+    have = getattr(teacher, "torch", None)
+    if have is not None and d is not None:
+        if have[0] != d:
             raise ValueError("the teacher's entries must be on the logits' GPU")
-        if teacher.torch[1] < x.rows:
-            raise ValueError("the teacher must have an entry list for each of %d rows" % x.rows)
+        if have[1] < n:
+            raise ValueError("the teacher must have an entry list for each of %d rows" % n)
     _check(lib().mp_distill_loss(ctypes.byref(x), ctypes.byref(teacher),
-                                 f(weights, torch.float32, "weights"),
-                                 f(loss, torch.float32, "loss"), _grad_of(x, grad),
-                                 _stream(stream)))
+                                 _array(weights, _F32, n, "weights", d),
+                                 _array(loss, _F32, n, "loss", d), _grad_of(x, grad),
+                                 _stream_of(stream, d)))
 
 
 # --- convenience ---------------------------------------------------------------

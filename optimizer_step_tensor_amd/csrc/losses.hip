@@ -725,7 +725,9 @@ __device__ __forceinline__ void stream_grad(const RowGrad& r, const typename Fmt
     for (; i < nvec; i += THREADS) one(load_vec<DT, NT>(body + int64_t(i) * E), i);
 }
 
-// The statistics alone, one row per workgroup.
+// The statistics alone, one row per workgroup.  Bound by HBM reads: 8192 x 128256
+// bf16 318 us, 6.6 TB/s; 2048 x 50304 38 us.  128, 512 or 1024 lanes and 2 or 8
+// vectors in flight are within 3% there, and slower for few or short rows.
 template <int DT, int THREADS, bool DISTILL>
 __global__ __launch_bounds__(THREADS) void k_rows_stats(LossArgs a)
 {
@@ -765,6 +767,12 @@ __global__ __launch_bounds__(THREADS) void k_rows_stats(LossArgs a)
 // gradient: NV vectors a lane, the first FULL of them inside the row for every
 // lane, all requested before the first is used.  REST: the row goes on past
 // them, and that part is read twice.
+//
+// Bound by HBM, in the pattern of one row per workgroup: 8192 x 128256 bf16, a
+// tenth of the rows off, 730 us, 5.5 TB/s (a bare copy in this shape 5.4-5.6; with
+// the exponentials left out the time is the same); 4096 x 50304 bf16 152 us, 5.4.
+// Reading the row a second time instead took 1185 us; a persistent workgroup that
+// requests the next row while it stores this one 880.
 template <int DT, int THREADS, int NV, int FULL, bool REST, bool DISTILL>
 __global__ __launch_bounds__(THREADS) void k_rows_held(LossArgs a)
 {
@@ -864,7 +872,8 @@ __global__ __launch_bounds__(THREADS) void k_rows_held(LossArgs a)
 // the workspace -- part 0 also takes what is read singly: the ends of the row,
 // the target's logit, the teacher's sums, all before any gradient is stored.  In
 // the second every workgroup joins its row's parts and stores its part of the
-// gradient; part 0 writes the outputs.
+// gradient; part 0 writes the outputs.  Two launches of 3-4 us each for one row of
+// 128256 bf16, 6 and 7 us for 61 (against 12 and 20 us as whole rows).
 constexpr int kPartThreads = 256;
 constexpr int kPartHeld = 4;                              // vectors a lane
 constexpr int kPartVecs = kPartThreads * kPartHeld;
@@ -1116,6 +1125,7 @@ __global__ __launch_bounds__(kGradThreads) void k_logprob_grad(LogitsView v, Gra
 
 // One workgroup per pair, in a fixed order: the two sequences' sums, the loss,
 // and dlogp of their rows; one more workgroup for the rows outside every sequence.
+// A launch's time and two memory latencies: 4-5 us for 8 pairs of 256 rows.
 constexpr int kPairThreads = 256;
 
 __device__ __forceinline__ int64_t clamp_row(int64_t r, int64_t rows)
@@ -1189,6 +1199,8 @@ __global__ __launch_bounds__(kPairThreads) void k_pairs(PairArgs a)
     }
 }
 
+// One workgroup, so that the count needs no cleared memory: 2-4 us for 8192
+// targets, a launch's time.
 constexpr int kCountThreads = 1024;
 
 __global__ __launch_bounds__(kCountThreads) void k_target_count(int64_t n, const int64_t* targets,
