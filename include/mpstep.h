@@ -504,7 +504,8 @@ mp_status mp_adamw_step_fp8(mp_plan* plan, mp_state* state, const mp_gradset* la
  *    written as zeros.  A target (or a teacher's id) >= vocab cannot be refused
  *    without a sync: no memory is read there, the row's loss, log-probability
  *    and gradient are NaN, and the step that they feed is skipped as on an overflow.
- *  - Logits of -inf (a vocabulary mask) have probability 0.  A row without a
+ *  - Logits of -inf (a vocabulary mask) have probability 0; where a loss needs
+ *    the logarithm of such a probability it is infinite.  A row without a
  *    finite logit, or with +inf or NaN, has no distribution: NaN results.
  *  - Statistics are held in fp32 with the sums over a row joined in binary64,
  *    in a fixed order (the same bits on every run); losses are formed in
@@ -519,8 +520,8 @@ mp_status mp_adamw_step_fp8(mp_plan* plan, mp_state* state, const mp_gradset* la
 /* fp32 logits; the 16-bit formats are MP_BF16 and MP_FP16.  Not a format of a plan. */
 #define MP_FP32 2
 
-/* Scratch that the calls may use to split rows over several workgroups when
- * there are few of them (at most 256); 16-byte aligned. */
+/* Scratch that the calls may use to split long rows over several workgroups
+ * when there are few of them; 16-byte aligned. */
 #define MP_LOSS_WORKSPACE_BYTES 65536
 
 /* `rows` rows of `vocab` logits, row r at element r * stride (stride >= vocab

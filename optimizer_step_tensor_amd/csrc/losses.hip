@@ -411,7 +411,8 @@ __device__ __forceinline__ double k3_of(double d)
         for (int i = 10; i >= 3; --i) p = __builtin_fmaf(t * (1.0f / i), p, 1.0f);
         return 0.5 * d * d * static_cast<double>(p);
     }
-    return exp_of(d) - d - 1.0;
+    const double e = exp_of(d);
+    return __builtin_isinf(e) ? e : e - d - 1.0;      // d = inf is not inf - inf
 }
 
 // exp(d) - 1 for d <= 0, with its digits near 0.

@@ -510,6 +510,32 @@ def test_policy_rows_at_extremes(mp):
     assert loss[3] == 0 and not torch.isnan(bd.t).any()
 
 
+def test_policy_target_that_is_masked(mp):
+    """A target's logit of -inf: lp = -inf, an infinite loss where there is a KL term (a finite one
+    where there is none: rho = 0), the other rows as ever."""
+    import torch
+    rng = gen(19)
+    x, t = make_x(rng, 4, 700, "bf16")
+    lp = ref.logprob(x, t)["logp"]
+    old, rf, adv = f32(lp), f32(lp + 0.1), f32([1.0, -1.0, 2.0, 1.0])
+    x[0, t[0]] = x[1, t[1]] = -np.inf
+    for kl_coef in (0.25, 0.0):
+        bx, bd, lx, lg, factor, keep = state_for(mp, x, "bf16")
+        loss, l2, kl = empty(4), empty(4), empty(4)
+        mp.mp_policy_loss(lx, dev(t), dev(old), dev(rf), dev(adv), None,
+                          mp.policy_cfg(0.25, 0.5, kl_coef), loss, l2, kl, lg)
+        assert bool(torch.isneginf(l2[:2]).all()) and bool(torch.isposinf(kl[:2]).all())
+        r = ref.policy(x[2:], t[2:], old[2:], rf[2:], adv[2:], 1.0, None, (0.25, 0.5), kl_coef, factor,
+                       "bf16")
+        check("loss", loss[2:], r["loss"], r["tol_loss"])
+        check("dx", bd.t[2:], r["dx"], r["tol_dx"])
+        if kl_coef:
+            assert bool(torch.isposinf(loss[:2]).all())
+            assert not bool(torch.isfinite(bd.t[:2].float()).all(1).any())
+        else:
+            assert loss[0] == 0.0 and loss[1] == 0.75 and not bd.t[:2].any()
+
+
 def test_preference_sequences_at_extremes(mp):
     """Empty sequences, sequences without a target, rows before, between and behind, starts out of
     range and decreasing (taken as the nearest, never followed)."""
@@ -681,6 +707,35 @@ def test_captured_and_replayed(mp, rows, V):
         graph.replay()
         torch.cuda.synchronize()
         same_bits(results(st), want)
+
+
+def test_two_graphs_that_share_a_workspace(mp):
+    """Two captured passes over different buffers and one workspace, replayed in turn on a stream."""
+    import torch
+    sts = [fresh(mp, 9, 60001, "bf16", 23), fresh(mp, 40, 131072, "fp16", 24)]
+    sts[1]["ws"] = sts[0]["ws"]
+    graphs = []
+    for st in sts:
+        everything(mp, st)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            everything(mp, st)
+    g = torch.Generator(device="cuda").manual_seed(78)
+    for _ in range(3):
+        want = []
+        for st in sts:
+            refill(st, g)
+            everything(mp, st)
+            want.append(results(st))
+            for d in st["dx"] + st["loss"]:
+                d.fill_(-3.0)
+        sts[0]["ws"].fill_(0x77)
+        for i in (0, 1, 0, 1, 1, 0):
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for st, w in zip(sts, want):
+            same_bits(results(st), w)
 
 
 def test_two_streams_at_once(mp):
