@@ -590,6 +590,7 @@ def mp_token_logprob(x, targets, logp, lse=None, stream=None):
 
 
 def mp_token_logprob_grad(x, targets, lse, dlogp, grad, stream=None):
+    """grad: logits_grad(...), written; lse from mp_token_logprob; dlogp: float32 [rows]."""
     n, d = _place(x)
     _check(lib().mp_token_logprob_grad(ctypes.byref(x), _array(targets, _I64, n, "targets", d),
                                        _array(lse, _F32, n, "lse", d),
@@ -598,6 +599,7 @@ def mp_token_logprob_grad(x, targets, lse, dlogp, grad, stream=None):
 
 
 def mp_cross_entropy(x, targets, weights, loss, grad=None, stream=None):
+    """loss: float32 [rows], written; weights: float32 [rows] or None."""
     n, d = _place(x)
     _check(lib().mp_cross_entropy(ctypes.byref(x), _array(targets, _I64, n, "targets", d),
                                   _array(weights, _F32, n, "weights", d),
@@ -607,6 +609,8 @@ def mp_cross_entropy(x, targets, weights, loss, grad=None, stream=None):
 
 def mp_policy_loss(x, targets, old_logp, ref_logp, advantage, weights, cfg, loss, logp=None,
                    kl=None, grad=None, stream=None):
+    """Per-row inputs float32 [rows] (ref_logp and weights may be None); cfg: policy_cfg(...);
+    loss, logp and kl: float32 [rows], written."""
     n, d = _place(x)
     _check(lib().mp_policy_loss(ctypes.byref(x), _array(targets, _I64, n, "targets", d),
                                 _array(old_logp, _F32, n, "old_logp", d),
@@ -620,6 +624,9 @@ def mp_policy_loss(x, targets, old_logp, ref_logp, advantage, weights, cfg, loss
 
 def mp_preference_loss(x, targets, n_pairs, seq_start, ref_logp, cfg, loss, seq_logp, logp, lse,
                        dlogp, grad=None, stream=None):
+    """seq_start: int64 [2 n_pairs + 1]; ref_logp: float32 [2 n_pairs] or None; cfg:
+    preference_cfg(...); loss [n_pairs], seq_logp [2 n_pairs], logp, lse and dlogp [rows]:
+    float32, written."""
     (n, d), p = _place(x), int(n_pairs)
     _check(lib().mp_preference_loss(ctypes.byref(x), _array(targets, _I64, n, "targets", d), p,
                                     _array(seq_start, _I64, 2 * p + 1, "seq_start", d),
@@ -632,6 +639,7 @@ def mp_preference_loss(x, targets, n_pairs, seq_start, ref_logp, cfg, loss, seq_
 
 
 def mp_distill_loss(x, teacher, weights, loss, grad=None, stream=None):
+    """teacher: teacher(...); loss: float32 [rows], written; weights: float32 [rows] or None."""
     n, d = _place(x)
     have = getattr(teacher, "torch", None)
     if have is not None and d is not None:
