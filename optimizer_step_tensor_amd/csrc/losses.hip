@@ -1322,10 +1322,14 @@ void rows_dt(LossArgs a, hipStream_t s)
     // a wave a row, unless a teacher's list needs more lanes: 30 rows of 3551 with 201 entries
     // 40 us with one wave, 8 us with four
     if (a.kind == kDistill && a.k > 64 && nvec <= 256 * 4) return held<DT, 256, 4, 0>(a, s);
-    if (nvec <= 64 * 4) return held<DT, 64, 4, 0>(a, s);
+    // (a lane's vectors past the row's end still take their arithmetic: 16384 x 1000 bf16 20.5 us
+    // with 2 vectors a lane, 24.5 with 4; 16384 x 10000 124 us with 6, 131 with 8)
+    if (nvec <= 64 * 2) return held<DT, 64, 2, 0>(a, s);
+    if (nvec <= 64 * 4) return held<DT, 64, 4, 2>(a, s);
     if (nvec <= 64 * 8) return held<DT, 64, 8, 4>(a, s);
     if (nvec <= 256 * 4) return held<DT, 256, 4, 2>(a, s);
-    if (nvec <= 256 * 8) return held<DT, 256, 8, 4>(a, s);
+    if (nvec <= 256 * 6) return held<DT, 256, 6, 4>(a, s);
+    if (nvec <= 256 * 8) return held<DT, 256, 8, 6>(a, s);
     // Up to 64 K (fp32: 32 K) logits, where two rows fit a compute unit.  16-bit logits have twice
     // the arithmetic per byte and gain from the smaller workgroup, whose waves wait less for each
     // other: 8192 x 20000 bf16 124 us against 137 with 1024 lanes, distillation over 4096 x

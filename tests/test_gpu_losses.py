@@ -220,6 +220,32 @@ def test_large_vocabularies(mp, kind, V):
     run_all(mp, kind, V, 2, 1.0, LAYOUTS[(i + 1) % 4], 200 + i, True)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("vecs", [128, 256, 512, 1024, 1536, 2048, 4096, 8192, 16384, 20480])
+def test_rows_that_fill_their_vectors(mp, kind, vecs):
+    """Exactly `vecs` 16-byte vectors, one more, and one more of which an odd start takes the first
+    (so that as many as before are left): the last and the first row lengths of a shape."""
+    per = 8 if kind == "bf16" else 4
+    for V, shift in ((per * vecs, 0), (per * vecs, 1), (per * (vecs + 1), 0), (per * (vecs + 1), 1),
+                     (per * (vecs + 1) + per - 1, per - 1)):
+        rng = gen(20, V, shift)
+        x, t = make_x(rng, 2, V, kind)
+        t[0] = V - 1 if shift else 0
+        bx, bd, lx, lg, factor, keep = state_for(mp, x, kind, shift=shift, dshift=shift)
+        loss = empty(2)
+        mp.mp_cross_entropy(lx, dev(t), None, loss, lg)
+        r = ref.cross_entropy(x, t, 1.0, None, factor, kind)
+        check((V, shift, "loss"), loss, r["loss"], r["tol_loss"])
+        check((V, shift, "dx"), bd.t, r["dx"], r["tol_dx"])
+        ids, vals = rng.integers(0, V, (2, 9)), f32(rng.normal(0, 1, (2, 9)))
+        ids[:, 0] = V - 1
+        mp.mp_distill_loss(lx, mp.teacher(dev(vals), dev(ids)), None, loss, lg)
+        r = ref.distill(x, vals, ids, None, 1.0, None, factor, kind)
+        check((V, shift, "distill loss"), loss, r["loss"], r["tol_loss"])
+        check((V, shift, "distill dx"), bd.t, r["dx"], r["tol_dx"])
+        assert bx.untouched() and bd.untouched()
+
+
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("rows", [33, 257, 1031])
 def test_many_rows(mp, kind, rows):
