@@ -1174,12 +1174,12 @@ __global__ __launch_bounds__(kPairThreads) void k_pairs(PairArgs a)
     const double delta = (pi[0] - ref[0]) - (pi[1] - ref[1]);
     double loss, slope;                 // dloss/dD
     if (a.kind == MP_PREF_SIGMOID) {
-        // -log sigmoid(+-h) = log(1 + exp(-|h|)) + max(-+h, 0)
+        // -log sigmoid(+-h) = log(1 + exp(-|h|)) + max(-+h, 0), the latter with weight 1 - eps below
+        // h = 0 and eps above; no weight leaves it out, infinite (a sequence of probability 0) or not
         const double h = a.beta * delta - a.margin;
         const double u = exp(-fabs(h));
-        const double soft = log1p(u);
-        loss = soft + (1.0 - a.label_smoothing) * (h < 0.0 ? -h : 0.0) +
-               a.label_smoothing * (h > 0.0 ? h : 0.0);
+        const double weight = h < 0.0 ? 1.0 - a.label_smoothing : a.label_smoothing;
+        loss = log1p(u) + (weight != 0.0 ? weight * fabs(h) : 0.0);
         const double sig_neg = h >= 0.0 ? u / (1.0 + u) : 1.0 / (1.0 + u);    // sigmoid(-h)
         slope = a.beta * (a.label_smoothing * (1.0 - sig_neg) - (1.0 - a.label_smoothing) * sig_neg);
     } else {
