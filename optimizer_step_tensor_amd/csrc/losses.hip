@@ -415,10 +415,10 @@ __device__ __forceinline__ double k3_of(double d)
     return __builtin_isinf(e) ? e : e - d - 1.0;      // d = inf is not inf - inf
 }
 
-// exp(d) - 1 for d <= 0, with its digits near 0.
+// exp(d) - 1, with its digits near 0 and without d itself far from it (-1 at d = -inf).
 __device__ __forceinline__ double expm1_of(double d)
 {
-    return d > -0.5 ? d + k3_of(d) : exp_of(d) - 1.0;
+    return __builtin_fabs(d) < 0.5 ? d + k3_of(d) : exp_of(d) - 1.0;
 }
 
 // What a row's formula takes besides the logits: requested when the row is, so
@@ -480,7 +480,7 @@ __device__ __forceinline__ double target_loss(const LossArgs& a, int64_t row, co
             const double c = static_cast<double>(a.kl_coef);
             if (c != 0.0) {
                 loss += c * kl;
-                slope -= c * (kl + d);
+                slope -= c * expm1_of(d);      // not kl + d: kl has lost the 1 where d is large
             }
         }
         loss *= w;

@@ -67,3 +67,65 @@ def test_squared_preference_with_a_masked_target(mp, kind):  # noqa: F811
     assert o[0].tolist() == [np.inf, np.inf]
     assert o[1][0] == -np.inf and o[1][3] == -np.inf
     del keep, bx, bd, factor
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("V,with_ws", [(700, False), (60001, True)])
+@pytest.mark.parametrize("low", [-np.inf, -3.4028234663852886e38, -1e18, -1e4])
+def test_policy_whose_reference_gives_the_token_nothing(mp, kind, V, with_ws, low):  # noqa: F811
+    """d = ref_logp - lp far below 0: exp(d) = 0, so kl = -d - 1 (infinite or finite as ref_logp is)
+    and its slope is kl_coef exactly; A = 0 leaves that alone, other rows add the policy's own."""
+    rows, kl_coef = 6, 0.25
+    x, t = make_x(gen(44, V), rows, V, kind)
+    parts = ref._target(x, t, 1.0)
+    lp, ds = parts[0], parts[4]
+    old, adv = f32(lp + 0.05), f32([0.0, 1.0, -1.0, 0.0, 0.5, -0.5])
+    w = f32([1.0, 1.0, 2.0, -1.0, 0.5, 1.0])
+    rf = np.full(rows, f32(low))
+    with np.errstate(all="ignore"):
+        kl = -(rf - lp) - 1.0
+    rho = np.exp(lp - old)          # e^-0.05: inside 0.8 .. 1.25, the ratio is not clipped
+    free, dl = rho * adv, ds + 3 * U
+    bx, bd, lx, lg, factor, keep = state_for(mp, x, kind, ws=workspace(mp) if with_ws else None)
+    loss, lp_out, kl_out = empty(rows), empty(rows), empty(rows)
+    mp.mp_policy_loss(lx, dev(t), dev(old), dev(rf), dev(adv), dev(w),
+                      mp.policy_cfg(0.2, 0.25, kl_coef), loss, lp_out, kl_out, lg)
+    err = np.abs(free) * (dl + 4 * U)
+    with np.errstate(all="ignore"):
+        check("kl", kl_out, kl, dl + ref.round_tol(kl))
+        want = w * (kl_coef * kl - free)
+        check("loss", loss, want, np.abs(w) * (err + kl_coef * dl) + ref.round_tol(want))
+    check("logp", lp_out, lp, dl + ref.round_tol(lp))
+    # the slope: kl_coef without an error of its own (1 - exp(d) is 1 to 2^-53)
+    dx, tol = ref.target_grad(x, t, 1.0, w * (kl_coef - free), np.abs(w) * err, factor, kind, parts)
+    check("dx", bd.t, dx, tol)
+    assert bx.untouched() and bd.untouched()
+    del keep
+
+
+def test_policy_kl_slope_over_its_range(mp):  # noqa: F811
+    """kl and its slope on both sides of |d| = 1/2 and far out, where A = 0: the target's element of
+    the gradient is kl_coef (1 - exp(d)) (1 - q_t), read back relative to its own size.  lp's error
+    dl (an exponential's (|t| + 2) 4u a term, the sum's and the logarithm's) enters d as it is; exp's
+    own is 2^-23 of exp(d), the series' below 2^-22 of its sum."""
+    V = 300
+    ds = np.concatenate([[0.5, -0.5], np.linspace(-0.75, 0.75, 31), [-2.0, 2.0, -9.0, 9.0, -40.0, 40.0]])
+    rows = len(ds)
+    x, t = make_x(gen(45), rows, V, "fp32", 1.0)
+    parts = ref._target(x, t, 1.0)
+    lp, dl = parts[0], parts[4] + 3 * U
+    rf = f32(lp + ds)
+    d = rf - lp
+    bx, bd, lx, lg, factor, keep = state_for(mp, x, "fp32")
+    loss, kl = empty(rows), empty(rows)
+    zero = dev(np.zeros(rows))
+    mp.mp_policy_loss(lx, dev(t), zero, dev(rf), zero, None, mp.policy_cfg(0.2, 0.2, 0.5), loss, None,
+                      kl, lg)
+    want = np.where(np.abs(d) < 1e-3, d * d / 2 * (1 + d / 3 * (1 + d / 4)), np.expm1(d) - d)
+    slope_err = np.exp(d) * (dl + 2 * U) + np.where(np.abs(d) < 0.6, want * 4 * U, 0.0)
+    tol = np.abs(np.expm1(d)) * dl + np.exp(np.maximum(d, 0)) * (dl * dl + 2 * U) * (np.abs(d) > 0.49)
+    check("kl", kl, want, tol + want * 4 * U + dl * dl + ref.round_tol(want))
+    dx, tol = ref.target_grad(x, t, 1.0, -0.5 * np.expm1(d), 0.5 * slope_err, factor, "fp32", parts)
+    check("dx", bd.t, dx, tol)
+    assert bx.untouched() and bd.untouched()
+    del keep, loss
