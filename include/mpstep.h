@@ -498,6 +498,11 @@ mp_status mp_adamw_step_fp8(mp_plan* plan, mp_state* state, const mp_gradset* la
  *  - Logits and gradients need the alignment of their element type only; row
  *    starts on 16 bytes (128 are better) let the vector accesses use whole
  *    lines.  The other arrays are contiguous, aligned to their element type.
+ *  - What a call writes -- its outputs, the gradient's rows, the workspace -- must
+ *    not overlap anything else of the same call, inputs included (else
+ *    MP_ERR_INVALID): some rows are shared by several workgroups, which read their
+ *    inputs while one of them writes.  The one exception is a gradient that
+ *    replaces the logits.  The padding between strided rows is free for other use.
  *  - A target below 0 (-100 by custom), or a weight of exactly 0, switches its
  *    row off: the row's logits and other inputs are not used (NaN and inf there
  *    do no harm), its loss and log-probability are 0 and its gradient row is

@@ -81,13 +81,79 @@ mp_status check_grad(const mp_logits* x, const mp_logits_grad* g)
     return MP_OK;
 }
 
-mp_status check_array(const void* p, uintptr_t align, int64_t rows, bool required, const char* name)
-{
-    if (required && rows > 0 && p == nullptr) return set_error(MP_ERR_INVALID, "%s is NULL", name);
-    if (!aligned(p, align))
-        return set_error(MP_ERR_ALIGN, "%s must be %d-byte aligned", name, static_cast<int>(align));
-    return MP_OK;
-}
+// The arrays of a call besides the logits and their gradient: each is checked as it is added, and
+// `disjoint` refuses what the kernels would read and write at once -- the parts of a split row read
+// the row's inputs while the first writes its outputs, and inputs are taken as constant.
+class Arrays {
+public:
+    mp_status in(const void* p, uintptr_t elem, int64_t n, bool required, const char* name)
+    {
+        return add(p, elem, n, required, false, name);
+    }
+    mp_status out(const void* p, uintptr_t elem, int64_t n, bool required, const char* name)
+    {
+        return add(p, elem, n, required, true, name);
+    }
+    mp_status disjoint(const mp_logits* x, const mp_logits_grad* g)
+    {
+        if (x->rows > 0) put(x->workspace, MP_LOSS_WORKSPACE_BYTES, true, "workspace");
+        if (g != nullptr) {
+            put(g->dev_scale, 4, false, "dev_scale");
+            put(g->dev_count, 8, false, "dev_count");
+        }
+        for (int i = 0; i < count_; ++i) {
+            const One& a = one_[i];
+            for (int j = 0; j < i; ++j) {
+                const One& b = one_[j];
+                if ((a.written || b.written) && a.at < b.at + b.bytes && b.at < a.at + a.bytes)
+                    return set_error(MP_ERR_INVALID, "%s overlaps %s", b.name, a.name);
+            }
+            if (a.written && in_rows(a, x->data, x->stride, x))
+                return set_error(MP_ERR_INVALID, "%s overlaps the logits", a.name);
+            if (g != nullptr && in_rows(a, g->data, g->stride, x))
+                return set_error(MP_ERR_INVALID, "%s overlaps the gradient", a.name);
+        }
+        return MP_OK;
+    }
+
+private:
+    struct One {
+        uintptr_t at, bytes;
+        const char* name;
+        bool written;
+    };
+    One one_[16];           // a policy loss has 11: 5 read, 3 written, the workspace, two scalars
+    int count_ = 0;
+
+    void put(const void* p, uintptr_t bytes, bool written, const char* name)
+    {
+        if (p != nullptr && bytes > 0)
+            one_[count_++] = One{reinterpret_cast<uintptr_t>(p), bytes, name, written};
+    }
+    mp_status add(const void* p, uintptr_t elem, int64_t n, bool required, bool written, const char* name)
+    {
+        if (required && n > 0 && p == nullptr) return set_error(MP_ERR_INVALID, "%s is NULL", name);
+        if (!aligned(p, elem))
+            return set_error(MP_ERR_ALIGN, "%s must be %d-byte aligned", name, static_cast<int>(elem));
+        put(p, static_cast<uintptr_t>(n) * elem, written, name);
+        return MP_OK;
+    }
+    // Does `a` meet one of the rows?  (What lies between them is not the call's.)
+    static bool in_rows(const One& a, const void* data, int64_t stride, const mp_logits* x)
+    {
+        if (x->rows == 0) return false;
+        const int es = elem_bytes(x->dtype);
+        const uintptr_t base = reinterpret_cast<uintptr_t>(data);
+        const uintptr_t row = static_cast<uintptr_t>(x->vocab) * es;
+        if (a.at >= base + extent(x->rows, x->vocab, x->rows > 1 ? stride : x->vocab, es) ||
+            a.at + a.bytes <= base)
+            return false;
+        if (a.at < base || x->rows == 1) return true;
+        const uintptr_t step = static_cast<uintptr_t>(stride) * es;
+        const uintptr_t within = (a.at - base) % step;
+        return within < row || within + a.bytes > step;
+    }
+};
 
 // The work is launched on the current device: `data` (the logits) has to live
 // there, and the stream, too.
@@ -161,8 +227,9 @@ extern "C" {
 mp_status mp_target_count(int64_t n, const int64_t* targets, int64_t* count, mp_stream stream)
 {
     if (n < 0) return set_error(MP_ERR_INVALID, "n must be >= 0");
-    mp_status st = check_array(targets, 8, n, true, "targets");
-    if (st == MP_OK) st = check_array(count, 8, 1, true, "count");
+    Arrays arrays;
+    mp_status st = arrays.in(targets, 8, n, true, "targets");
+    if (st == MP_OK) st = arrays.out(count, 8, 1, true, "count");
     if (st == MP_OK) st = check_place(count, "count", stream);
     if (st != MP_OK) return st;
     hipError_t e = mpk::launch_target_count(n, targets, count, static_cast<hipStream_t>(stream));
@@ -174,9 +241,11 @@ mp_status mp_token_logprob(const mp_logits* x, const int64_t* targets, float* lo
                            mp_stream stream)
 {
     mp_status st = check_logits(x);
-    if (st == MP_OK) st = check_array(targets, 8, x->rows, true, "targets");
-    if (st == MP_OK) st = check_array(logp, 4, x->rows, true, "logp");
-    if (st == MP_OK) st = check_array(lse, 4, x->rows, false, "lse");
+    Arrays arrays;
+    if (st == MP_OK) st = arrays.in(targets, 8, x->rows, true, "targets");
+    if (st == MP_OK) st = arrays.out(logp, 4, x->rows, true, "logp");
+    if (st == MP_OK) st = arrays.out(lse, 4, x->rows, false, "lse");
+    if (st == MP_OK) st = arrays.disjoint(x, nullptr);
     if (st != MP_OK) return st;
     LossArgs a{};
     a.kind = mpk::kLogprob;
@@ -192,9 +261,11 @@ mp_status mp_token_logprob_grad(const mp_logits* x, const int64_t* targets, cons
     mp_status st = check_logits(x);
     if (st == MP_OK && grad == nullptr) st = set_error(MP_ERR_INVALID, "grad is NULL");
     if (st == MP_OK) st = check_grad(x, grad);
-    if (st == MP_OK) st = check_array(targets, 8, x->rows, true, "targets");
-    if (st == MP_OK) st = check_array(lse, 4, x->rows, true, "lse");
-    if (st == MP_OK) st = check_array(dlogp, 4, x->rows, true, "dlogp");
+    Arrays arrays;
+    if (st == MP_OK) st = arrays.in(targets, 8, x->rows, true, "targets");
+    if (st == MP_OK) st = arrays.in(lse, 4, x->rows, true, "lse");
+    if (st == MP_OK) st = arrays.in(dlogp, 4, x->rows, true, "dlogp");
+    if (st == MP_OK) st = arrays.disjoint(x, grad);
     if (st != MP_OK) return st;
     if (x->rows == 0) return set_ok();
     st = check_place(x->data, "logits", stream);
@@ -210,9 +281,11 @@ mp_status mp_cross_entropy(const mp_logits* x, const int64_t* targets, const flo
 {
     mp_status st = check_logits(x);
     if (st == MP_OK) st = check_grad(x, grad);
-    if (st == MP_OK) st = check_array(targets, 8, x->rows, true, "targets");
-    if (st == MP_OK) st = check_array(weights, 4, x->rows, false, "weights");
-    if (st == MP_OK) st = check_array(loss, 4, x->rows, true, "loss");
+    Arrays arrays;
+    if (st == MP_OK) st = arrays.in(targets, 8, x->rows, true, "targets");
+    if (st == MP_OK) st = arrays.in(weights, 4, x->rows, false, "weights");
+    if (st == MP_OK) st = arrays.out(loss, 4, x->rows, true, "loss");
+    if (st == MP_OK) st = arrays.disjoint(x, grad);
     if (st != MP_OK) return st;
     LossArgs a{};
     a.kind = mpk::kXent;
@@ -239,14 +312,16 @@ mp_status mp_policy_loss(const mp_logits* x, const int64_t* targets, const float
         return set_error(MP_ERR_INVALID, "kl_coef must be finite and >= 0");
     if (x->rows > 0 && ref_logp == nullptr && (cfg->kl_coef != 0.0f || kl != nullptr))
         return set_error(MP_ERR_INVALID, "a KL term needs ref_logp");
-    st = check_array(targets, 8, x->rows, true, "targets");
-    if (st == MP_OK) st = check_array(old_logp, 4, x->rows, true, "old_logp");
-    if (st == MP_OK) st = check_array(ref_logp, 4, x->rows, false, "ref_logp");
-    if (st == MP_OK) st = check_array(advantage, 4, x->rows, true, "advantage");
-    if (st == MP_OK) st = check_array(weights, 4, x->rows, false, "weights");
-    if (st == MP_OK) st = check_array(loss, 4, x->rows, true, "loss");
-    if (st == MP_OK) st = check_array(logp, 4, x->rows, false, "logp");
-    if (st == MP_OK) st = check_array(kl, 4, x->rows, false, "kl");
+    Arrays arrays;
+    st = arrays.in(targets, 8, x->rows, true, "targets");
+    if (st == MP_OK) st = arrays.in(old_logp, 4, x->rows, true, "old_logp");
+    if (st == MP_OK) st = arrays.in(ref_logp, 4, x->rows, false, "ref_logp");
+    if (st == MP_OK) st = arrays.in(advantage, 4, x->rows, true, "advantage");
+    if (st == MP_OK) st = arrays.in(weights, 4, x->rows, false, "weights");
+    if (st == MP_OK) st = arrays.out(loss, 4, x->rows, true, "loss");
+    if (st == MP_OK) st = arrays.out(logp, 4, x->rows, false, "logp");
+    if (st == MP_OK) st = arrays.out(kl, 4, x->rows, false, "kl");
+    if (st == MP_OK) st = arrays.disjoint(x, grad);
     if (st != MP_OK) return st;
     LossArgs a{};
     a.kind = mpk::kPolicy;
@@ -283,14 +358,16 @@ mp_status mp_preference_loss(const mp_logits* x, const int64_t* targets, int64_t
     if (!std::isfinite(cfg->margin)) return set_error(MP_ERR_INVALID, "margin must be finite");
     if (n_pairs < 1 || n_pairs > kMaxRows)
         return set_error(MP_ERR_INVALID, "n_pairs must be 1 to 2^22 - 1");
-    st = check_array(targets, 8, x->rows, true, "targets");
-    if (st == MP_OK) st = check_array(seq_start, 8, 1, true, "seq_start");
-    if (st == MP_OK) st = check_array(ref_logp, 4, 1, false, "ref_logp");
-    if (st == MP_OK) st = check_array(loss, 4, 1, true, "loss");
-    if (st == MP_OK) st = check_array(seq_logp, 4, 1, true, "seq_logp");
-    if (st == MP_OK) st = check_array(logp, 4, x->rows, true, "logp");
-    if (st == MP_OK) st = check_array(lse, 4, x->rows, true, "lse");
-    if (st == MP_OK) st = check_array(dlogp, 4, x->rows, true, "dlogp");
+    Arrays arrays;
+    st = arrays.in(targets, 8, x->rows, true, "targets");
+    if (st == MP_OK) st = arrays.in(seq_start, 8, 2 * n_pairs + 1, true, "seq_start");
+    if (st == MP_OK) st = arrays.in(ref_logp, 4, 2 * n_pairs, false, "ref_logp");
+    if (st == MP_OK) st = arrays.out(loss, 4, n_pairs, true, "loss");
+    if (st == MP_OK) st = arrays.out(seq_logp, 4, 2 * n_pairs, true, "seq_logp");
+    if (st == MP_OK) st = arrays.out(logp, 4, x->rows, true, "logp");
+    if (st == MP_OK) st = arrays.out(lse, 4, x->rows, true, "lse");
+    if (st == MP_OK) st = arrays.out(dlogp, 4, x->rows, true, "dlogp");
+    if (st == MP_OK) st = arrays.disjoint(x, grad);
     if (st == MP_OK) st = check_place(x->rows > 0 ? x->data : seq_start,
                                       x->rows > 0 ? "logits" : "seq_start", stream);
     if (st != MP_OK) return st;
@@ -335,11 +412,14 @@ mp_status mp_distill_loss(const mp_logits* x, const mp_teacher* teacher, const f
     if (teacher->k < 1 || teacher->k > MP_DISTILL_MAX_K)
         return set_error(MP_ERR_INVALID, "teacher: k must be 1 to %d", MP_DISTILL_MAX_K);
     if (!known_dtype(teacher->dtype)) return set_error(MP_ERR_INVALID, "teacher: unknown dtype");
-    st = check_array(teacher->values, elem_bytes(teacher->dtype), x->rows, true, "teacher values");
-    if (st == MP_OK) st = check_array(teacher->ids, 8, x->rows, true, "teacher ids");
-    if (st == MP_OK) st = check_array(teacher->lse, 4, x->rows, false, "teacher lse");
-    if (st == MP_OK) st = check_array(weights, 4, x->rows, false, "weights");
-    if (st == MP_OK) st = check_array(loss, 4, x->rows, true, "loss");
+    Arrays arrays;
+    const int64_t entries = x->rows * teacher->k;
+    st = arrays.in(teacher->values, elem_bytes(teacher->dtype), entries, true, "teacher values");
+    if (st == MP_OK) st = arrays.in(teacher->ids, 8, entries, true, "teacher ids");
+    if (st == MP_OK) st = arrays.in(teacher->lse, 4, x->rows, false, "teacher lse");
+    if (st == MP_OK) st = arrays.in(weights, 4, x->rows, false, "weights");
+    if (st == MP_OK) st = arrays.out(loss, 4, x->rows, true, "loss");
+    if (st == MP_OK) st = arrays.disjoint(x, grad);
     if (st != MP_OK) return st;
     LossArgs a{};
     a.kind = mpk::kDistill;
