@@ -515,7 +515,10 @@ mp_status mp_adamw_step_fp8(mp_plan* plan, mp_state* state, const mp_gradset* la
  *  - Statistics are held in fp32 with the sums over a row joined in binary64,
  *    in a fixed order (the same bits on every run); losses are formed in
  *    binary64 and rounded once; a gradient is formed in fp32 and rounded once
- *    (round to nearest even) to the logits' type.
+ *    (round to nearest even) to the logits' type.  So a log-probability's error
+ *    is absolute (at worst 2^-15 for 2^17 logits, in proportion beyond), not
+ *    relative to itself: one of size below 2^-24 may come out as 0, and the
+ *    target's element of the gradient with it.
  *  - rows = 0 is allowed and enqueues nothing (but the pairs of a preference loss).
  *  - The logits (the count, of mp_target_count) and the stream must belong to
  *    the current device (else MP_ERR_INVALID).  Nothing is allocated; the calls

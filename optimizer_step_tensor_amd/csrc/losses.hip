@@ -5,8 +5,10 @@
 // A lane keeps a running (m, s) over its share of the row -- s is rescaled when
 // m grows, so the row is read once -- and the shares are joined in binary64 in
 // a fixed order.  What a loss needs of the row is then a handful of numbers:
-// the target's log-probability (m and ln s enter it apart, so a probability
-// near 1 keeps its digits) or the k teacher entries.  The gradient of every loss
+// the target's log-probability (m and ln s enter it apart: a probability near 1 keeps
+// the digits that s has -- a part of 2^-24 that lies in the lane of the row's
+// maximum is lost in that lane's fp32 sum, in another lane it counts down to 2^-52)
+// or the k teacher entries.  The gradient of every loss
 // here is dx_j = a q_j, with a few elements (the target, the teacher's ids) that take
 // another value: these are stored over the dense ones afterwards.
 //
