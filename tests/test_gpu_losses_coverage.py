@@ -1,102 +1,23 @@
 """Every logit of a row counts, in every shape of the row kernels, and the variants that read large
-logits past the caches: against binary64, with tolerances from the additions that a lane makes.
-
-u = 2^-24 is half a step of fp32.  A row is shared by at least 64 lanes, from 512 vectors on by 256;
-a lane adds its vectors in pairs -- the 2 E elements of a pair one after another, then to its running
-sum, which is rescaled (exp2: 2 u, a product: u, the sum: u) -- and up to four single ones (a head or
-tail element, the vectors that are left over).  That bounds a row's sum by
-
-    chain = (2 E + 4 (ceil(vectors / (2 lanes)) + 5) + 8) u
-
-relative, the 8 for the joins.  An exponent has three roundings, exp2 one step: E_j = 4 u (|z_j| + 2) of
-a share, z = (x - m) / T, so a sum is off by at most ds = sum_j q_j E_j + chain, and so is lp, besides
-3 u of the logarithm.  At 128256 16-bit logits chain is 1.0e-5, where eight average logits are 6e-5.
-"""
+logits past the caches: against binary64, with tolerances from the additions that a lane makes
+(loss_rows.py)."""
 import numpy as np
 import pytest
 
-from loss_reference import FLUSH, HALF_STEP, TINY, U
-from test_gpu_losses import KINDS, LAYOUTS, Buf, empty, gen, mp, ttype, workspace  # noqa: F401
+from loss_rows import HALF_STEP, U, E, borders, chain_of, near, planted, reference
+from test_gpu_losses import KINDS, LAYOUTS, Buf, empty, mp, ttype, workspace  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
-E = {"bf16": 8, "fp16": 8, "fp32": 4}
 
-
-def reference(x, t, kind, factor, T=1.0, from_lse=False):
-    """Cross-entropy of the rows of a device tensor in binary64: loss, lse, dx and how far each may
-    be off.  from_lse: dx formed of an lse that was rounded to fp32, as mp_token_logprob_grad's is."""
+def planted_rows(V, kind, layout, key):
+    """planted() in a guarded tensor; the targets are elsewhere."""
     import torch
-    x = x.double()
-    rows, V = x.shape
-    at = torch.arange(rows, device="cuda")
-    m = x.amax(1, keepdim=True)
-    z = (x - m) / T
-    e = torch.exp(z)
-    s = e.sum(1, keepdim=True)
-    q = e / s
-    ln_s = torch.log(s)[:, 0]
-    lse = m[:, 0] / T + ln_s
-    live = t >= 0
-    tt = t.clamp(min=0)
-    nvec = V // E[kind]
-    lanes = 64 if nvec <= 512 else 256
-    chain = (2 * E[kind] + 4 * (-(-nvec // (2 * lanes)) + 5) + 8) * U
-    Ej = 4 * U * (z.abs() + 2.0)
-    ds = (q * Ej).sum(1) + chain
-    lp = z[at, tt] - ln_s
-    r = dict(loss=torch.where(live, -lp, 0.0), lse=torch.where(live, lse, 0.0))
-    r["tol_loss"] = torch.where(live, ds + 3 * U + lp.abs() * U, 0.0)
-    r["tol_lse"] = torch.where(live, ds + 3 * U + lse.abs() * U, 0.0)
-    if from_lse:
-        # lse's rounding is an error of every exponent; for 16-bit results the exponent has one more
-        # rounding of the size of x / T, and k's own correction is left out (2 u)
-        ds = ds + 3 * U + lse.abs() * U * (4 if kind != "fp32" else 2)
-        if kind != "fp32":
-            Ej = Ej + 4 * U * x.abs() / T
-    c = factor / T
-    dx = c * q
-    tol = abs(c) * q * (Ej + ds[:, None] + 8 * U) + abs(c) * FLUSH
-    dx[at, tt] = c * torch.expm1(lp)
-    tol[at, tt] += abs(c) * (4 * U + (2 * torch.exp(lp) * ds if from_lse else 0.0))
-    r["dx"] = torch.where(live[:, None], dx, 0.0)
-    r["tol_dx"] = torch.where(live[:, None], tol * 1.01, 0.0) + r["dx"].abs() * HALF_STEP[kind] + TINY[kind]
-    return r
-
-
-def near(name, got, want, tol):
-    import torch
-    off = (got.double() - want).abs()
-    bad = ~(off <= tol)
-    assert not bool(bad.any()), (name, int(bad.sum()), bad.nonzero()[:4].tolist(),
-                                 float((off / tol.clamp(min=1e-300)).max()))
-    assert bool(torch.isfinite(want).all())
-
-
-def borders(V, kind):
-    """Where a row is cut: its ends, and the borders of every lane count's vectors."""
-    per = E[kind]
-    at = set(range(min(V, per + 2))) | set(range(max(0, V - 2 * per - 2), V))
-    for lanes in (64, 256, 512, 1024):
-        step = lanes * per
-        n = V // step
-        for j in {1, 2, n // 2, n - 1, n}:
-            at |= {j * step - 1, j * step, j * step + per - 1}
-    return sorted(p for p in at if 0 <= p < V)
-
-
-def planted(V, kind, layout, key):
-    """A row for each border, with a logit there that holds about half of the row's mass; the target
-    is elsewhere.  Left out of the statistics it would move the loss by ln 2."""
-    import torch
-    at = borders(V, kind)
-    rows = len(at)
+    rows = len(borders(V, kind))
     g = torch.Generator(device="cuda").manual_seed(key)
-    lay = {k: v for k, v in layout.items() if k in ("pad", "shift")}
-    bx = Buf(rows, V, kind, **lay)
+    bx = Buf(rows, V, kind, layout.get("pad", 0), layout.get("shift", 0))
     bx.t.copy_(torch.randn(rows, V, generator=g, device="cuda"))
-    p = torch.tensor(at, device="cuda")
-    bx.t[torch.arange(rows, device="cuda"), p] = float(np.round(np.log(1.65 * V) * 4) / 4)
+    p = torch.tensor(planted(bx.t, kind), device="cuda")
     t = (p + 1 + torch.randint(V - 1, (rows,), generator=g, device="cuda")) % V
     return bx, t
 
@@ -108,13 +29,14 @@ SHAPES = {"bf16": [40, 1003, 1900, 3999, 8190, 12003, 16385, 20011, 31001, 40003
           "fp32": [20, 500, 1003, 2001, 4003, 6001, 8190, 16001, 24001, 32001, 40003, 48005, 57000,
                    65531, 81001, 90003, 262147]}
 CASES = [(k, V) for k, vs in SHAPES.items() for V in vs] + [("fp16", V) for V in (1003, 50305, 128256)]
+assert {k for k, _ in CASES} == set(KINDS)
 
 
 @pytest.mark.parametrize("kind,V", CASES)
 def test_no_logit_is_left_out(mp, kind, V):  # noqa: F811
     i = CASES.index((kind, V))
     layout = LAYOUTS[i % 4]
-    bx, t = planted(V, kind, layout, 50 + i)
+    bx, t = planted_rows(V, kind, layout, 50 + i)
     x = bx.t.clone()
     rows = x.shape[0]
     r = reference(x, t, kind, 2.0)
@@ -224,8 +146,7 @@ def test_digits_of_a_probability_near_one(mp, kind, V, with_ws, with_grad):  # n
     binary64: down to 2^-52); in one lane's vector an fp32 sum holds both, and the loss and the
     target's gradient are right to chain, absolutely."""
     gaps = np.array([8.0, 12.0, 20.0, 28.0])
-    per = E[kind]
-    chain = (2 * per + 4 * (-(-(V // per) // 512) + 5) + 8) * U if V > 1000 else (2 * per + 4 * 9 + 8) * U
+    per, chain = E[kind], chain_of(V, kind)
     import torch
     for far in (True, False):
         x = torch.full((4, V), float("-inf"), dtype=ttype(kind), device="cuda")
