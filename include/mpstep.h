@@ -513,9 +513,12 @@ mp_status mp_adamw_step_fp8(mp_plan* plan, mp_state* state, const mp_gradset* la
  *    the logarithm of such a probability it is infinite.  A row without a
  *    finite logit, or with +inf or NaN, has no distribution: NaN results.
  *  - Statistics are held in fp32 with the sums over a row joined in binary64,
- *    in a fixed order (the same bits on every run); losses are formed in
- *    binary64 and rounded once; a gradient is formed in fp32 and rounded once
- *    (round to nearest even) to the logits' type.  So a log-probability's error
+ *    in a fixed order (the same bits on every run); a teacher's sums are held
+ *    alike.  Losses are formed of them in binary64 and rounded once to fp32, with
+ *    exponentials (the ratio rho, exp(d), the teacher's shares) of 24 bits; a
+ *    preference loss adds the log-probabilities as its output logp holds them,
+ *    rounded to fp32.  A gradient is formed in fp32 and rounded once (round to
+ *    nearest even) to the logits' type.  So a log-probability's error
  *    is absolute (at worst 2^-15 for 2^17 logits, in proportion beyond), not
  *    relative to itself: one of size below 2^-24 may come out as 0, and the
  *    target's element of the gradient with it.
@@ -577,9 +580,10 @@ mp_status mp_token_logprob(const mp_logits* x, const int64_t* targets, float* lo
  * mp_token_logprob on the same logits:
  *   dx_rj = scale/T * dlogp[r] * ((j = t) - q_rj).
  * A row with dlogp[r] == 0 is written as zeros without being read.  q is as
- * exact as lse is in fp32: where |lse| is 1000, to 3e-5; an lse beyond 2e38 (a
- * row of nothing but the type's lowest value) gives a gradient that is not
- * finite.  The fused calls below have no such limit. */
+ * exact as lse is in fp32: where |lse| is 1000, to 3e-5 (16-bit logits: 2e-4,
+ * less than half a step of the result, and in proportion to |lse| from there); an
+ * lse beyond 2e38 (a row of nothing but the type's lowest value) gives a gradient
+ * that is not finite.  The fused calls below have no such limit. */
 mp_status mp_token_logprob_grad(const mp_logits* x, const int64_t* targets, const float* lse,
                                 const float* dlogp, const mp_logits_grad* grad, mp_stream stream);
 
@@ -629,7 +633,8 @@ typedef struct {
  * seq_start[i + 1] - 1, pair p the chosen sequence p and the rejected sequence
  * n_pairs + p.  seq_start: 2 n_pairs + 1 int64 in device memory, not
  * decreasing, 0 <= seq_start[i] <= rows (a value outside is taken as the
- * nearest of these, a sequence that would end before it starts as empty).
+ * nearest of these, a sequence that would end before it starts as empty; where
+ * starts that decrease give a row to two sequences, its dlogp is that of either).
  * With pi_i the sum (mean) of lp over the targets of sequence i -- 0 if it has
  * none -- and ref_logp[i] the reference's (NULL: 0):
  *   D = (pi_p - ref_p) - (pi_{p+n} - ref_{p+n});   h = beta D - margin
