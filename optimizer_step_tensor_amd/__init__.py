@@ -577,6 +577,8 @@ _F32, _I64 = torch.float32, torch.int64
 def mp_target_count(targets, count, n=None, stream=None):
     """count[0] = how many targets (int64, the first n or all) are >= 0."""
     n = targets.numel() if n is None else int(n)
+    if hasattr(targets, "device") and hasattr(count, "device") and targets.device != count.device:
+        raise ValueError("targets and count must be on one GPU")
     _check(lib().mp_target_count(n, _array(targets, _I64, n, "targets"),
                                  _array(count, _I64, 1, "count"), _stream(stream)))
 

@@ -172,3 +172,27 @@ def test_arrays_side_by_side(mp):
             for got, ref in zip((loss, logp, kl, wide[:, :V]), want + [dx]):
                 assert torch.allclose(got, ref, rtol=1e-5, atol=1e-6)
             assert torch.equal(flat[:4 * rows], per_row.flatten())
+
+
+def test_targets_and_their_count_live_on_one_gpu(mp):
+    """The kernel runs where the count lives; targets of another GPU are refused by the binding."""
+    import torch
+
+    class OnGpu:
+        dtype, is_cuda = torch.int64, True
+
+        def __init__(self, device, n):
+            self.device, self.n = torch.device("cuda", device), n
+
+        def numel(self):
+            return self.n
+
+        def is_contiguous(self):
+            return True
+
+        def data_ptr(self):
+            return 3 * STEP
+    with pytest.raises(ValueError, match="one GPU"):
+        mp.mp_target_count(OnGpu(1, 4), OnGpu(0, 1), stream=0)
+    with pytest.raises(mp.MpError):             # as far as the library: no such memory
+        mp.mp_target_count(OnGpu(0, 4), OnGpu(0, 1), stream=0)
