@@ -513,8 +513,8 @@ mp_status mp_adamw_step_fp8(mp_plan* plan, mp_state* state, const mp_gradset* la
  *    the logarithm of such a probability it is infinite.  A row without a
  *    finite logit, or with +inf or NaN, has no distribution: NaN results.
  *  - Statistics are held in fp32 with the sums over a row joined in binary64,
- *    in a fixed order (the same bits on every run); a teacher's sums are held
- *    alike.  Losses are formed of them in binary64 and rounded once to fp32, with
+ *    in a fixed order (the same bits on every run), a teacher's sums in binary64.
+ *    Losses are formed of them in binary64 and rounded once to fp32, with
  *    exponentials (the ratio rho, exp(d), the teacher's shares) of 24 bits; a
  *    preference loss adds the log-probabilities as its output logp holds them,
  *    rounded to fp32.  A gradient is formed in fp32 and rounded once (round to

@@ -217,19 +217,18 @@ __device__ __forceinline__ void add(Acc& a, const float (&f)[N], float k_hi, flo
     a.m = g;
 }
 
-// A lane's share of a teacher's entries: the running maximum of v, and the sums
-// of e = exp2((v - m) k) and e (v - x), x being the student's logit at the entry.
-struct TeacherAcc {
-    float m = -FLT_MAX;
-    float s = 0.0f;
-    float c = 0.0f;
+// The largest of a teacher's values v and of the student's logits x at its entries:
+// the sums over the entries are formed relative to both.
+struct TeacherMax {
+    float v = -FLT_MAX;
+    float x = -__builtin_inff();
 };
 
 struct Stat {
     float m;          // the row's maximum, the sum relative to it
     double s;
-    float tm;         // the teacher's, with distillation
-    double ts, tc;
+    float tm, xm;     // with distillation: the largest v and x of the list, the sums of
+    double ts, tc;    // e = exp2((v - tm) k) and e ((v - tm) - (x - xm))
 };
 
 // A lane's value and its partner's D lanes away, for reductions whose earlier steps
@@ -286,63 +285,55 @@ __device__ __forceinline__ double lanes_sum(double v)
     return v;
 }
 
-// (m, s[]) joined over groups of WIDTH lanes.  An infinite sum (a share of the
-// teacher's where the student has none) that is scaled to nothing is nothing; NaN
-// stays.
-template <int WIDTH, int N>
-__device__ __forceinline__ void join_lanes(float& m, double (&s)[N], float k_hi, float k_lo)
+// (m, s) joined over groups of WIDTH lanes.
+template <int WIDTH>
+__device__ __forceinline__ void join_lanes(float& m, double& s, float k_hi, float k_lo)
 {
     const float own = m;
     m = lanes_max<WIDTH>(m);
-    const double scale = static_cast<double>(exp2_hw(scaled(own, m, k_hi, k_lo)));
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        s[i] = lanes_sum<WIDTH>(scale == 0.0 && __builtin_isinf(s[i]) ? 0.0 : s[i] * scale);
-    }
+    s = lanes_sum<WIDTH>(s * static_cast<double>(exp2_hw(scaled(own, m, k_hi, k_lo))));
 }
 
 // Join every lane's share; the result is valid in the first wave, whose lanes
-// alone go on to the row's formula.
+// alone go on to the row's formula.  The teacher's sums are not formed yet; what the
+// lanes have put in shared memory is there for them.
 template <int THREADS, bool DISTILL>
-__device__ __forceinline__ Stat join(const Acc& a, const TeacherAcc& t, float k_hi, float k_lo)
+__device__ __forceinline__ Stat join(const Acc& a, const TeacherMax& t, float k_hi, float k_lo)
 {
     constexpr int W = THREADS / kWave;
-    __shared__ float m[2][W];
-    __shared__ double s[3][W];
-    Stat r;
-    double one[1] = {static_cast<double>(a.s)};
-    double two[2] = {static_cast<double>(t.s), static_cast<double>(t.c)};
+    __shared__ float m[3][W];
+    __shared__ double s[W];
+    Stat r{};
     r.m = a.m;
-    r.tm = t.m;
-    join_lanes<kWave>(r.m, one, k_hi, k_lo);
-    if constexpr (DISTILL) join_lanes<kWave>(r.tm, two, k_hi, k_lo);
+    r.s = static_cast<double>(a.s);
+    join_lanes<kWave>(r.m, r.s, k_hi, k_lo);
+    if constexpr (DISTILL) {
+        r.tm = lanes_max<kWave>(t.v);
+        r.xm = lanes_max<kWave>(t.x);
+    }
     if constexpr (W > 1) {
         const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
         if (lane == 0) {
             m[0][wave] = r.m;
-            s[0][wave] = one[0];
+            s[wave] = r.s;
             if constexpr (DISTILL) {
                 m[1][wave] = r.tm;
-                s[1][wave] = two[0];
-                s[2][wave] = two[1];
+                m[2][wave] = r.xm;
             }
         }
         __syncthreads();
         if (wave == 0) {
             r.m = m[0][lane % W];
-            one[0] = s[0][lane % W];
-            join_lanes<W>(r.m, one, k_hi, k_lo);
+            r.s = s[lane % W];
+            join_lanes<W>(r.m, r.s, k_hi, k_lo);
             if constexpr (DISTILL) {
-                r.tm = m[1][lane % W];
-                two[0] = s[1][lane % W];
-                two[1] = s[2][lane % W];
-                join_lanes<W>(r.tm, two, k_hi, k_lo);
+                r.tm = lanes_max<W>(m[1][lane % W]);
+                r.xm = lanes_max<W>(m[2][lane % W]);
             }
         }
+    } else if constexpr (DISTILL) {
+        __syncthreads();
     }
-    r.s = one[0];
-    r.ts = two[0];
-    r.tc = two[1];
     return r;
 }
 
@@ -526,11 +517,12 @@ __device__ __forceinline__ float teacher_value(const LossArgs& a, int64_t i)
 
 // The teacher's side of one row.  Every lane takes entries tid, tid + THREADS, ..: the first is
 // requested apart (`take`), so that its id is there early and the student's logit at it can be
-// on its way while the row is read.  ids (absent or past the vocabulary: -1), values and the
-// student's logits end up in shared memory for the stores over the dense gradient.
+// on its way while the row is read.  ids (absent: -1, past the vocabulary: kPast), values and the
+// student's logits end up in shared memory for the sums and the stores over the dense gradient.
 template <int DT, int THREADS>
 struct TeacherRow {
     using T = typename Fmt<DT>::T;
+    static constexpr int kPast = -2;
     const LossArgs& a;
     const T* x;
     int64_t base;
@@ -558,25 +550,40 @@ struct TeacherRow {
     {
         r.x = widen<DT>(x[r.id >= 0 && r.id < a.x.vocab ? r.id : 0]);
     }
-    __device__ __forceinline__ void put(TeacherAcc& acc, const Entry& r, int e) const
+    __device__ __forceinline__ void put(TeacherMax& top, const Entry& r, int e) const
     {
         if (e >= a.k) {
             if (e < padded(a.k)) id[e] = -1;
             return;
         }
         const bool in = r.id >= 0 && r.id < a.x.vocab;
-        id[e] = in ? static_cast<int32_t>(r.id) : -1;
+        id[e] = in ? static_cast<int32_t>(r.id) : r.id < 0 ? -1 : kPast;
         v[e] = r.v;
         xs[e] = r.x;
-        if (r.id >= a.x.vocab) acc.s = __builtin_nanf("");
         if (!in) return;
-        const float m = __builtin_fmaxf(acc.m, r.v);
-        const float old = exp2_hw(scaled(acc.m, m, a.x.k_hi, a.x.k_lo));
-        const float p = exp2_hw(scaled(r.v, m, a.x.k_hi, a.x.k_lo));
-        acc.m = m;
-        acc.s = acc.s * old + p;
-        acc.c = old != 0.0f ? acc.c * old : 0.0f;
-        if (p != 0.0f) acc.c += p * (r.v - r.x);      // a share of 0 adds 0 whatever the student has
+        top.v = __builtin_fmaxf(top.v, r.v);
+        top.x = __builtin_fmaxf(top.x, r.x);
+    }
+    // The sums over the list, by the lanes of the first wave after `join`: differences of logits
+    // in binary64, so that what all of a list have in common (the type's lowest value, at worst)
+    // costs nothing.
+    __device__ __forceinline__ void sums(Stat& st) const
+    {
+        if (st.xm == -__builtin_inff()) st.xm = 0.0f;      // the student has none of them: any finite
+        const double tm = static_cast<double>(st.tm), xm = static_cast<double>(st.xm);
+        double ts = 0.0, tc = 0.0;
+        for (int e = threadIdx.x; e < a.k; e += kWave) {
+            const int i = id[e];
+            if (i == kPast) ts = __builtin_nan("");
+            if (i < 0) continue;
+            const float p = exp2_hw(scaled(v[e], st.tm, a.x.k_hi, a.x.k_lo));
+            const double share = static_cast<double>(p);
+            ts += share;
+            // a share of 0 adds 0 whatever the student has
+            if (p != 0.0f) tc += share * ((static_cast<double>(v[e]) - tm) - (static_cast<double>(xs[e]) - xm));
+        }
+        st.ts = lanes_sum<kWave>(ts);
+        st.tc = lanes_sum<kWave>(tc);
     }
 };
 
@@ -615,28 +622,30 @@ __device__ __forceinline__ RowGrad row_formula(const LossArgs& a, int64_t row, c
     __shared__ RowGrad out;
     if (threadIdx.x < kWave) {
         const double ln_s = log_sum(st.s);
-        const double lse = static_cast<double>(st.m) * a.x.inv_t + ln_s;
         const double w = in.w, factor = in.factor;
         double mult;
         RowGrad r{};
         if constexpr (DISTILL) {
-            // With its own normaliser the shares sum to 1 and the loss is
-            // E_p[(v - x) / T] - norm + lse; a given one scales them all.
-            const double top = static_cast<double>(st.tm) * a.x.inv_t;
-            double norm = top + log_sum(st.ts), one = 1.0 / st.ts;
+            // log p_e = (v_e - tm) / T + at and log q_e = (x_e - xm) / T + log_q, at = -ln ts with the
+            // list's own normaliser (the shares sum to 1; a given one scales them all): only
+            // differences of logits enter, whatever their size.
+            double at = -log_sum(st.ts), one = 1.0 / st.ts;
             if (a.teacher_lse != nullptr) {
-                norm = static_cast<double>(in.teacher_lse);
-                one = exp_of(top - norm);
+                at = static_cast<double>(st.tm) * a.x.inv_t - static_cast<double>(in.teacher_lse);
+                one = exp_of(at);
             }
             const double mass = a.teacher_lse != nullptr ? st.ts * one : 1.0;
             r.off = st.ts == 0.0 || mass == 0.0;
-            const double loss = st.tc * one * a.x.inv_t + mass * (lse - norm);
+            const double log_q =
+                (static_cast<double>(st.xm) - static_cast<double>(st.m)) * a.x.inv_t - ln_s;
+            const double loss = st.tc * one * a.x.inv_t + mass * (at - log_q);
             if (writes && threadIdx.x == 0) a.loss[row] = static_cast<float>(w * loss);
             mult = factor * w * mass;
             if (!(st.ts >= 0.0)) mult = __builtin_nan("");
             r.tm = st.tm;
             r.share = static_cast<float>(factor * w * one);
         } else {
+            const double lse = static_cast<double>(st.m) * a.x.inv_t + ln_s;
             const double lp = (static_cast<double>(xt) - static_cast<double>(st.m)) * a.x.inv_t - ln_s;
             mult = -factor * target_loss(a, row, in, lp, lse, writes && threadIdx.x == 0);
             if (in.target >= a.x.vocab) mult = __builtin_nan("");
@@ -755,15 +764,16 @@ __global__ __launch_bounds__(THREADS) void k_rows_stats(LossArgs a)
     }
     if (a.x.stream) stream_stats<DT, THREADS, true>(acc, x + sp.head, 0, sp.nvec, a.x.k_hi, a.x.k_lo);
     else stream_stats<DT, THREADS, false>(acc, x + sp.head, 0, sp.nvec, a.x.k_hi, a.x.k_lo);
-    TeacherAcc tacc;
+    TeacherMax top;
     if constexpr (DISTILL) {
         for (int e = threadIdx.x; e < t.padded(a.k); e += THREADS) {
             auto entry = t.take(e);
             t.look_up(entry);
-            t.put(tacc, entry, e);
+            t.put(top, entry, e);
         }
     }
-    const Stat st = join<THREADS, DISTILL>(acc, tacc, a.x.k_hi, a.x.k_lo);
+    Stat st = join<THREADS, DISTILL>(acc, top, a.x.k_hi, a.x.k_lo);
+    if (DISTILL && threadIdx.x < kWave) t.sums(st);
     const RowGrad r = row_formula<THREADS, DISTILL>(a, row, in, st, xt);
     if (DISTILL && r.off) off_row<DT, THREADS>(a, row, nullptr);
 }
@@ -840,16 +850,17 @@ __global__ __launch_bounds__(THREADS) void k_rows_held(LossArgs a)
     }
     if constexpr (REST)
         stream_stats<DT, THREADS, false>(acc, x + sp.head, NV * THREADS, sp.nvec, k_hi, k_lo);
-    TeacherAcc tacc;
+    TeacherMax top;
     if constexpr (DISTILL) {
-        t.put(tacc, entry, tid);
+        t.put(top, entry, tid);
         for (int e = tid + THREADS; e < t.padded(a.k); e += THREADS) {
             entry = t.take(e);
             t.look_up(entry);
-            t.put(tacc, entry, e);
+            t.put(top, entry, e);
         }
     }
-    const Stat st = join<THREADS, DISTILL>(acc, tacc, k_hi, k_lo);
+    Stat st = join<THREADS, DISTILL>(acc, top, k_hi, k_lo);
+    if (DISTILL && tid < kWave) t.sums(st);
     const RowGrad r = row_formula<THREADS, DISTILL>(a, row, in, st, xt);
     if (DISTILL && r.off) return off_row<DT, THREADS>(a, row, dx);
     if constexpr (REST)
@@ -892,8 +903,8 @@ struct PartSum {
 
 struct PartRow {
     double ts, tc;
-    float tm, xt;
-    double unused;
+    float tm, xm;
+    float xt, unused;
 };
 
 // Workspace of a split launch: rows * parts PartSum, then rows PartRow.
@@ -916,8 +927,9 @@ __global__ __launch_bounds__(kPartThreads) void k_part_stats(LossArgs a, Parts w
     if (target < 0 || (a.weights != nullptr && read_table(a.weights + row) == 0.0f)) return;
     const void* align = a.g.dx != nullptr ? static_cast<const T*>(a.g.dx) + row * a.g.stride : x;
     const Span<DT> sp(align, n);
+    const TeacherRow<DT, kPartThreads> t(a, row, x, lds);
     Acc acc;
-    TeacherAcc tacc;
+    TeacherMax top;
     float xt = 0.0f;
     if (part == 0) {
         const int one = sp.single(threadIdx.x);
@@ -926,11 +938,10 @@ __global__ __launch_bounds__(kPartThreads) void k_part_stats(LossArgs a, Parts w
             add(acc, f, a.x.k_hi, a.x.k_lo);
         }
         if constexpr (DISTILL) {
-            const TeacherRow<DT, kPartThreads> t(a, row, x, lds);
             for (int e = threadIdx.x; e < a.k; e += kPartThreads) {
                 auto entry = t.take(e);
                 t.look_up(entry);
-                t.put(tacc, entry, e);
+                t.put(top, entry, e);
             }
         } else {
             xt = target < n ? widen<DT>(x[target]) : __builtin_nanf("");
@@ -939,10 +950,11 @@ __global__ __launch_bounds__(kPartThreads) void k_part_stats(LossArgs a, Parts w
     const int lo = part * w.vecs;
     stream_stats<DT, kPartThreads, false>(acc, x + sp.head, lo, min(lo + w.vecs, sp.nvec), a.x.k_hi,
                                           a.x.k_lo);
-    const Stat st = join<kPartThreads, DISTILL>(acc, tacc, a.x.k_hi, a.x.k_lo);
+    Stat st = join<kPartThreads, DISTILL>(acc, top, a.x.k_hi, a.x.k_lo);
+    if (DISTILL && part == 0 && threadIdx.x < kWave) t.sums(st);
     if (threadIdx.x == 0) {
         w.sum[row * w.parts + part] = PartSum{st.s, st.m, 0.0f};
-        if (part == 0) w.row[row] = PartRow{st.ts, st.tc, st.tm, xt, 0.0};
+        if (part == 0) w.row[row] = PartRow{st.ts, st.tc, st.tm, st.xm, xt, 0.0f};
     }
 }
 
@@ -986,7 +998,7 @@ __global__ __launch_bounds__(kPartThreads) void k_part_grad(LossArgs a, Parts w)
     const TeacherRow<DT, kPartThreads> t(a, row, x, lds);
     if constexpr (DISTILL) {
         if (dx != nullptr) {
-            TeacherAcc unused;
+            TeacherMax unused;
             for (int e = tid; e < t.padded(a.k); e += kPartThreads) {
                 auto entry = t.take(e);
                 // the ids that lie in this part: nobody else stores there
@@ -999,19 +1011,19 @@ __global__ __launch_bounds__(kPartThreads) void k_part_grad(LossArgs a, Parts w)
             }
         }
     }
-    Stat st{-FLT_MAX, 0.0, 0.0f, 0.0, 0.0};
+    Stat st{};
+    st.m = -FLT_MAX;
     float xt = 0.0f;
     if (tid < kWave) {
-        double sum[1] = {0.0};
         if (tid < w.parts) {
             const PartSum p = w.sum[row * w.parts + tid];
             st.m = p.m;
-            sum[0] = p.s;
+            st.s = p.s;
         }
-        join_lanes<kWave>(st.m, sum, k_hi, k_lo);
-        st.s = sum[0];
+        join_lanes<kWave>(st.m, st.s, k_hi, k_lo);
         const PartRow r = w.row[row];
         st.tm = r.tm;
+        st.xm = r.xm;
         st.ts = r.ts;
         st.tc = r.tc;
         xt = r.xt;
