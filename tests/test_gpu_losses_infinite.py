@@ -129,3 +129,33 @@ def test_policy_kl_slope_over_its_range(mp):  # noqa: F811
     check("dx", bd.t, dx, tol)
     assert bx.untouched() and bd.untouched()
     del keep, loss
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("V,with_ws", [(9, False), (1000, False), (9001, False), (60001, True)])
+def test_log_probabilities_under_a_mask(mp, kind, V, with_ws):  # noqa: F811
+    """-inf and the type's lowest value at half of the ids, one id left, the target masked: the
+    log-probability, and its gradient from the stored lse, in place, too."""
+    import torch
+    from test_gpu_losses import ttype
+    rng = gen(46, V)
+    x, t = make_x(rng, 4, V, kind)
+    mask = rng.random((4, V)) < 0.5
+    mask[np.arange(4), t] = False
+    x[0][mask[0]] = -np.inf
+    x[1][mask[1]] = float(torch.finfo(ttype(kind)).min)
+    x[2], x[2, t[2]] = -np.inf, 3.0
+    x[3, t[3]] = -np.inf
+    d = f32(rng.normal(0, 1, 4))
+    for inplace in (False, True):
+        bx, bd, lx, lg, factor, keep = state_for(mp, x, kind, 0.5, inplace=inplace, pad=1, dpad=1,
+                                                 ws=workspace(mp) if with_ws else None)
+        lp, lse = empty(4), empty(4)
+        mp.mp_token_logprob(lx, dev(t), lp, lse)
+        mp.mp_token_logprob_grad(lx, dev(t), lse, dev(d), lg)
+        r = ref.logprob(x, t, 0.5, d, factor, kind)
+        for k, v in (("logp", lp), ("lse", lse), ("dx", bd.t)):
+            assert not np.isnan(r["tol_" + k]).any()
+            check(k, v, r[k], r["tol_" + k])
+        assert lp[3] == -np.inf and bx.untouched() and bd.untouched()
+        del keep
