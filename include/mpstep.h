@@ -673,6 +673,70 @@ typedef struct {
 mp_status mp_distill_loss(const mp_logits* x, const mp_teacher* teacher, const float* weights,
                           float* loss, const mp_logits_grad* grad, mp_stream stream);
 
+/* ------------------------------------------------------------------------
+ * Scores of logits: what sampling reports of a distribution, what an entropy
+ * bonus takes, and the lists that mp_distill_loss reads.
+ *
+ * The conventions of the losses hold (types, alignment, overlaps, switched-off
+ * rows, rows without a distribution, places); logits->workspace is not used.
+ * ------------------------------------------------------------------------ */
+
+/* Entries per row that mp_token_score lists at most. */
+#define MP_SCORE_MAX_TOP 128
+
+/* Scratch that mp_token_score may use to split long rows over several
+ * workgroups when there are few of them; 16-byte aligned. */
+#define MP_SCORE_WORKSPACE_BYTES 1048576
+
+/* Outputs of mp_token_score; each may be NULL, but one of the first three or the
+ * lists (top > 0, then top_ids) must be there.  logp, lse and entropy: rows fp32.
+ * The lists: rows x top (0 <= top <= MP_SCORE_MAX_TOP), entry e of row r at
+ * r * top + e.  workspace: NULL, or MP_SCORE_WORKSPACE_BYTES of device memory, used
+ * as the losses use theirs. */
+typedef struct {
+    float* logp;
+    float* lse;
+    float* entropy;
+    int64_t* top_ids;
+    float* top_logp;
+    float* top_values;
+    void* workspace;
+    int32_t top;
+} mp_score;
+
+/* Of every row, with z = x / temperature and q = exp(z - lse):
+ *   logp[r]    = z_rt - lse_r of the target t          (targets: rows int64)
+ *   lse[r]     = log sum_j exp(z_rj)
+ *   entropy[r] = -sum_j q_rj log q_rj                  (q = 0 adds 0)
+ * and the `top` entries of the largest logits, the largest first and of equal ones
+ * (-0 and 0 are equal) the lowest id first: top_ids, their log-probabilities
+ * top_logp and the logits themselves, top_values (fp32 holds all three formats).
+ * A logit of -inf is no entry.  Where a row has fewer entries than `top`, the
+ * rest have id -1 and value and log-probability -inf; so have all of a
+ * switched-off row (its logp, lse and entropy are 0) and of a row without a
+ * distribution (those are NaN).  A target >= vocab makes logp NaN and changes
+ * nothing else.  targets may be NULL with logp: then no row is switched off.
+ *
+ * With top_values, top_ids and lse (or NULL) an mp_teacher of dtype MP_FP32 is
+ * what mp_distill_loss takes.
+ *
+ * Sums over a row are fp32 in a lane and joined in binary64: lse, entropy and log-probabilities
+ * have absolute errors like the losses' (a few 2^-24, more in proportion to the row's
+ * length); an entropy is at least 0.  The order of the entries is exact. */
+mp_status mp_token_score(const mp_logits* x, const int64_t* targets, const mp_score* out,
+                         mp_stream stream);
+
+/* The gradient of sum_r (dlogp[r] * lp_r + dentropy[r] * H_r) for any dlogp and
+ * dentropy, from the lse and entropy of mp_token_score on the same logits:
+ *   dx_rj = scale/T * (dlogp[r] * ((j = t) - q_rj) - dentropy[r] * q_rj (log q_rj + H_r)).
+ * dlogp (with targets) or dentropy (with entropy) may be NULL, for none of that
+ * part; targets may be given without dlogp, to switch rows off.  A row where both
+ * are 0 is written as zeros without being read.  An element with q_rj = 0 takes
+ * none of the entropy's part.  q is as exact as in mp_token_logprob_grad. */
+mp_status mp_token_score_grad(const mp_logits* x, const int64_t* targets, const float* lse,
+                              const float* entropy, const float* dlogp, const float* dentropy,
+                              const mp_logits_grad* grad, mp_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

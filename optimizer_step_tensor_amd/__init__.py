@@ -37,6 +37,7 @@ ENTRY_POINTS = [
     "mp_norm_partial_group", "mp_update_step_noalloc", "mp_accumulate_first_counts",
     "mp_target_count", "mp_token_logprob", "mp_token_logprob_grad", "mp_cross_entropy",
     "mp_policy_loss", "mp_preference_loss", "mp_distill_loss",
+    "mp_token_score", "mp_token_score_grad",
 ]
 
 MP_STATE_BLOB_BYTES = 256
@@ -44,6 +45,8 @@ MP_NOALLOC_MAX_NORM_BLOCKS = 262144
 MP_LOSS_WORKSPACE_BYTES = 65536
 MP_DISTILL_MAX_K = 1024
 MP_PREF_SIGMOID, MP_PREF_SQUARED = range(2)
+MP_SCORE_MAX_TOP = 128
+MP_SCORE_WORKSPACE_BYTES = 1 << 20
 
 
 class MpError(RuntimeError):
@@ -104,6 +107,13 @@ class PreferenceCfg(ctypes.Structure):
 class Teacher(ctypes.Structure):
     _fields_ = [("values", ctypes.c_void_p), ("ids", ctypes.c_void_p), ("lse", ctypes.c_void_p),
                 ("k", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class Score(ctypes.Structure):
+    _fields_ = [("logp", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("entropy", ctypes.c_void_p),
+                ("top_ids", ctypes.c_void_p), ("top_logp", ctypes.c_void_p),
+                ("top_values", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("top", ctypes.c_int32)]
 
 
 _lib = None
@@ -173,6 +183,8 @@ def _bind(L):
         "mp_policy_loss": ([P] * 12, i32),
         "mp_preference_loss": ([P, P, i64] + [P] * 10, i32),
         "mp_distill_loss": ([P, P, P, P, P, P], i32),
+        "mp_token_score": ([P, P, P, P], i32),
+        "mp_token_score_grad": ([P] * 8, i32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -653,6 +665,68 @@ def mp_distill_loss(x, teacher, weights, loss, grad=None, stream=None):
                                  _array(weights, _F32, n, "weights", d),
                                  _array(loss, _F32, n, "loss", d), _grad_of(x, grad),
                                  _stream_of(stream, d)))
+
+
+# --- scores of logits -------------------------------------------------------------
+
+def score(logp=None, lse=None, entropy=None, top_ids=None, top_logp=None, top_values=None,
+          workspace=None):
+    """The mp_score of float32 [rows] tensors (each may be None) and of the lists: int64 [rows, top]
+    ids, float32 [rows, top] log-probabilities and logits.  workspace: MP_SCORE_WORKSPACE_BYTES
+    uint8, used where there are few rows.  The struct keeps the tensors it describes."""
+    have = [t for t in (logp, lse, entropy, top_ids, top_logp, top_values) if t is not None]
+    if not have:
+        raise ValueError("a score needs an output")
+    rows, d, top = have[0].shape[0], have[0].device, 0
+    if top_ids is not None:
+        if top_ids.dim() != 2:
+            raise ValueError("top_ids must be a [rows, top] tensor")
+        top = top_ids.shape[1]
+    for t, name in ((top_logp, "top_logp"), (top_values, "top_values")):
+        if t is not None and (top_ids is None or t.shape != top_ids.shape):
+            raise ValueError("%s must have the shape of top_ids" % name)
+    if not have[0].is_cuda:
+        raise ValueError("the score must be on a GPU")
+    n = rows * top
+    out = Score(_array(logp, _F32, rows, "logp", d), _array(lse, _F32, rows, "lse", d),
+                _array(entropy, _F32, rows, "entropy", d), _array(top_ids, _I64, n, "top_ids", d),
+                _array(top_logp, _F32, n, "top_logp", d),
+                _array(top_values, _F32, n, "top_values", d),
+                _array(workspace, torch.uint8, MP_SCORE_WORKSPACE_BYTES, "workspace", d), top)
+    out.torch = (d, rows)
+    out.keep = (logp, lse, entropy, top_ids, top_logp, top_values, workspace)
+    return out
+
+
+def _fits(x, out, what):
+    """The rows and the GPU of outputs made of tensors are those of the logits x."""
+    have = getattr(out, "torch", None)
+    n, d = _place(x)
+    if have is not None and d is not None:
+        if have[0] != d:
+            raise ValueError("%s must be on the logits' GPU" % what)
+        if have[1] < n:
+            raise ValueError("%s must have %d rows" % (what, n))
+    return n, d
+
+
+def mp_token_score(x, targets, score, stream=None):
+    """x: logits(...); targets: int64 [rows], or None; score: score(...), its arrays written."""
+    n, d = _fits(x, score, "the score")
+    _check(lib().mp_token_score(ctypes.byref(x), _array(targets, _I64, n, "targets", d),
+                                ctypes.byref(score), _stream_of(stream, d)))
+
+
+def mp_token_score_grad(x, targets, lse, entropy, dlogp, dentropy, grad, stream=None):
+    """grad: logits_grad(...), written; lse and entropy from mp_token_score; dlogp and dentropy:
+    float32 [rows], either may be None."""
+    n, d = _place(x)
+    _check(lib().mp_token_score_grad(ctypes.byref(x), _array(targets, _I64, n, "targets", d),
+                                     _array(lse, _F32, n, "lse", d),
+                                     _array(entropy, _F32, n, "entropy", d),
+                                     _array(dlogp, _F32, n, "dlogp", d),
+                                     _array(dentropy, _F32, n, "dentropy", d), _grad_of(x, grad),
+                                     _stream_of(stream, d)))
 
 
 # --- convenience ---------------------------------------------------------------

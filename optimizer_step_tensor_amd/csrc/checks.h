@@ -91,6 +91,13 @@ public:
     {
         return add(p, elem, n, required, true, name);
     }
+    // a caller's optional scratch memory, which no call without rows touches
+    mp_status scratch(const void* p, uintptr_t bytes, int64_t rows)
+    {
+        if (!aligned(p, 16)) return set_error(MP_ERR_ALIGN, "the workspace must be 16-byte aligned");
+        if (rows > 0) put(p, bytes, true, "workspace");
+        return MP_OK;
+    }
     mp_status disjoint(const mp_logits* x, const mp_logits_grad* g)
     {
         if (x->rows > 0) put(x->workspace, MP_LOSS_WORKSPACE_BYTES, true, "workspace");
