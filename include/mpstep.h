@@ -737,6 +737,94 @@ mp_status mp_token_score_grad(const mp_logits* x, const int64_t* targets, const 
                               const float* entropy, const float* dlogp, const float* dentropy,
                               const mp_logits_grad* grad, mp_stream stream);
 
+/* ------------------------------------------------------------------------
+ * Routing to experts: from a router's logits the experts of every token and
+ * their weights, what balances the experts, and the logits' gradient.
+ *
+ * The logits are an mp_logits of rows = tokens and vocab = experts (at most
+ * MP_ROUTE_MAX_EXPERTS; temperature 1; logits->workspace is not used), the gradient an
+ * mp_logits_grad.  The conventions of the losses hold for types, alignment,
+ * overlaps and places.  mask: rows bytes, 0 for a token that is not routed, or
+ * NULL: its logits are not used, its weights are 0, its ids -1, its gradient 0.
+ * ------------------------------------------------------------------------ */
+#define MP_ROUTE_MAX_EXPERTS 1024
+#define MP_ROUTE_MAX_GROUPS 64
+#define MP_ROUTE_MAX_TOP 16
+#define MP_ROUTE_WORKSPACE_BYTES 4194304
+#define MP_ROUTE_SOFTMAX 0
+#define MP_ROUTE_SIGMOID 1
+
+/* Scores s = softmax(x) or sigmoid(x) of a token; selection scores c = s + bias.
+ * groups > 1: experts/groups consecutive experts are a group, it counts as the sum
+ * of its group_best (1 or 2) largest c, and only the top_groups largest groups (equal
+ * ones: the lowest first) are open.  Of the open experts the `top` largest c are
+ * chosen (equal ones: the lowest number first; 1 <= top <= MP_ROUTE_MAX_TOP, at most
+ * the experts of top_groups groups).  The weights are their s, divided by
+ * (their sum + 1e-20) where renormalise != 0, times scale. */
+typedef struct {
+    int32_t score;          /* MP_ROUTE_SOFTMAX or MP_ROUTE_SIGMOID */
+    int32_t top;
+    int32_t groups;         /* 1 to MP_ROUTE_MAX_GROUPS, a divisor of the experts */
+    int32_t top_groups;     /* 1 to groups */
+    int32_t group_best;
+    int32_t renormalise;
+    float scale;
+} mp_route_cfg;
+
+/* weights (fp32) and ids: rows x top.  For training also, each or NULL (share
+ * needs load, aux needs share): load, experts + 1 int64: how many tokens each expert
+ * got, then how many tokens were routed; share, experts fp32: the mean over these
+ * tokens of p = s (softmax) or s / sum s (sigmoid); aux, 2 fp32: the losses
+ * balance = experts sum_e load_e share_e / (top load[experts]) and the mean of
+ * lse^2 (0 for sigmoid scores).  workspace: with load, MP_ROUTE_WORKSPACE_BYTES of
+ * device memory, 16-byte aligned, used as the losses use theirs. */
+typedef struct {
+    float* weights;
+    int64_t* ids;
+    int64_t* load;
+    float* share;
+    float* aux;
+    void* workspace;
+} mp_routed;
+
+/* c and the groups' sums are formed in binary64 and compared after rounding to 42 bits.
+ * An expert whose logit is -inf, or whose bias is -inf or NaN, is closed; a logit of
+ * -inf has s = 0.  A sigmoid below 2^-1000 is 0, and p = 0 where all of a token's
+ * are.  A token with fewer open experts than `top` has ids -1 and weights 0 at its
+ * end; one with none is not among the tokens routed.  A token without a distribution (a NaN; with softmax
+ * also +inf, or nothing but -inf) has ids -1 and weights NaN and is in no sum.
+ * bias: experts fp32, or NULL: 0. */
+mp_status mp_route(const mp_logits* x, const float* bias, const uint8_t* mask,
+                   const mp_route_cfg* cfg, const mp_routed* out, mp_stream stream);
+
+/* The gradient of
+ *   sum dweights * weights + f (balance_coef * balance + z_coef * mean lse^2),
+ * f = grad->scale * (*dev_scale) / (*dev_count), with ids held and load as
+ * counted: dweights carries its own factors, f is of the two losses.  ids and load from
+ * mp_route on the same logits, mask and cfg (load may be NULL where both coefficients
+ * are 0; loads of several calls, added up by the caller, balance over all of them).
+ * dweights: rows x top fp32, or NULL.  The losses act on tokens with an id >= 0;
+ * a token without one has a gradient of 0, or NaN without a distribution.  An id
+ * >= experts makes the token's gradient NaN, and no memory is read there; an id that
+ * comes twice counts twice.  z_coef must be 0 with sigmoid scores.  Formed in
+ * fp32 (a sigmoid below 2^-126 is 0), with sums over a token in binary64, and
+ * rounded once. */
+mp_status mp_route_grad(const mp_logits* x, const uint8_t* mask, const mp_route_cfg* cfg,
+                        const int64_t* ids, const float* dweights, const int64_t* load,
+                        float balance_coef, float z_coef, const mp_logits_grad* grad,
+                        mp_stream stream);
+
+/* The balancing bias after an update, for `layers` routers at once:
+ *   out_e = bias_e + speed * sign(sum_j load_j / experts - load_e),
+ * one fp32 addition, with load the sum of n_loads arrays of layers x (experts + 1)
+ * int64 (a micro-batch's loads each; the last of a layer's does not count).  bias and
+ * out: layers x experts fp32, out may be bias.  state: NULL, or out = bias where the state's last
+ * check found an overflow (found_inf), as the other parameters stay where the step is
+ * skipped; call it behind the norm pass on the same stream. */
+mp_status mp_route_bias_update(int32_t layers, int32_t experts, const float* bias, int32_t n_loads,
+                               const int64_t* load, float speed, float* out, const mp_state* state,
+                               mp_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -37,7 +37,7 @@ ENTRY_POINTS = [
     "mp_norm_partial_group", "mp_update_step_noalloc", "mp_accumulate_first_counts",
     "mp_target_count", "mp_token_logprob", "mp_token_logprob_grad", "mp_cross_entropy",
     "mp_policy_loss", "mp_preference_loss", "mp_distill_loss",
-    "mp_token_score", "mp_token_score_grad",
+    "mp_token_score", "mp_token_score_grad", "mp_route", "mp_route_grad", "mp_route_bias_update",
 ]
 
 MP_STATE_BLOB_BYTES = 256
@@ -47,6 +47,9 @@ MP_DISTILL_MAX_K = 1024
 MP_PREF_SIGMOID, MP_PREF_SQUARED = range(2)
 MP_SCORE_MAX_TOP = 128
 MP_SCORE_WORKSPACE_BYTES = 1 << 20
+MP_ROUTE_MAX_EXPERTS, MP_ROUTE_MAX_GROUPS, MP_ROUTE_MAX_TOP = 1024, 64, 16
+MP_ROUTE_WORKSPACE_BYTES = 4 << 20
+MP_ROUTE_SOFTMAX, MP_ROUTE_SIGMOID = range(2)
 
 
 class MpError(RuntimeError):
@@ -114,6 +117,16 @@ class Score(ctypes.Structure):
                 ("top_ids", ctypes.c_void_p), ("top_logp", ctypes.c_void_p),
                 ("top_values", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
                 ("top", ctypes.c_int32)]
+
+
+class RouteCfg(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("score", "top", "groups", "top_groups", "group_best",
+                                              "renormalise")] + [("scale", ctypes.c_float)]
+
+
+class Routed(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("weights", "ids", "load", "share", "aux",
+                                               "workspace")]
 
 
 _lib = None
@@ -185,6 +198,9 @@ def _bind(L):
         "mp_distill_loss": ([P, P, P, P, P, P], i32),
         "mp_token_score": ([P, P, P, P], i32),
         "mp_token_score_grad": ([P] * 8, i32),
+        "mp_route": ([P] * 6, i32),
+        "mp_route_grad": ([P] * 6 + [f32, f32, P, P], i32),
+        "mp_route_bias_update": ([i32, i32, P, i32, P, f32, P, P, P], i32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -727,6 +743,89 @@ def mp_token_score_grad(x, targets, lse, entropy, dlogp, dentropy, grad, stream=
                                      _array(dlogp, _F32, n, "dlogp", d),
                                      _array(dentropy, _F32, n, "dentropy", d), _grad_of(x, grad),
                                      _stream_of(stream, d)))
+
+
+# --- routing to experts ------------------------------------------------------------
+
+def route_cfg(top, score=MP_ROUTE_SOFTMAX, groups=1, top_groups=1, group_best=1, renormalise=True,
+              scale=1.0):
+    return RouteCfg(score, top, groups, top_groups, group_best, int(bool(renormalise)), scale)
+
+
+def routed(weights, ids, load=None, share=None, aux=None, workspace=None):
+    """The mp_routed of [tokens, top] tensors, float32 weights and int64 ids, and for training of
+    load (int64 [experts + 1]), share (float32 [experts]), aux (float32 [2]) and a workspace of
+    MP_ROUTE_WORKSPACE_BYTES uint8.  The struct keeps the tensors it describes."""
+    if ids.dim() != 2 or weights.shape != ids.shape:
+        raise ValueError("weights and ids must be [tokens, top] tensors")
+    if not ids.is_cuda:
+        raise ValueError("ids must be on a GPU")
+    d, n = ids.device, ids.numel()
+    out = Routed(_array(weights, _F32, n, "weights", d), _array(ids, _I64, n, "ids", d),
+                 _array(load, _I64, 1, "load", d), _array(share, _F32, 1, "share", d),
+                 _array(aux, _F32, 2, "aux", d),
+                 _array(workspace, torch.uint8, MP_ROUTE_WORKSPACE_BYTES, "workspace", d))
+    out.torch = (d, ids.shape[0])
+    out.shape = (ids.shape[1], None if load is None else load.numel(),
+                 None if share is None else share.numel())
+    out.keep = (weights, ids, load, share, aux, workspace)
+    return out
+
+
+def _mask(mask, n, device):
+    """Address of a mask of n torch.bool or uint8."""
+    bool_ = isinstance(mask, torch.Tensor) and mask.dtype is torch.bool
+    return _array(mask, torch.bool if bool_ else torch.uint8, n, "mask", device)
+
+
+def mp_route(x, bias, mask, cfg, routed, stream=None):
+    """x: logits(...) of [tokens, experts]; bias: float32 [experts] or None; mask: bool or uint8
+    [tokens] or None; cfg: route_cfg(...); routed: routed(...), its arrays written."""
+    n, d = _fits(x, routed, "what is routed")
+    shape = getattr(routed, "shape", None)
+    if shape is not None:
+        if shape[0] != cfg.top:
+            raise ValueError("weights and ids must have %d columns" % cfg.top)
+        for have, want, name in ((shape[1], x.vocab + 1, "load"), (shape[2], x.vocab, "share")):
+            if have is not None and have < want:
+                raise ValueError("%s must have %d elements" % (name, want))
+    _check(lib().mp_route(ctypes.byref(x), _array(bias, _F32, x.vocab, "bias", d),
+                          _mask(mask, n, d), ctypes.byref(cfg), ctypes.byref(routed),
+                          _stream_of(stream, d)))
+
+
+def mp_route_grad(x, mask, cfg, ids, dweights, load, balance_coef, z_coef, grad, stream=None):
+    """ids and dweights: int64 and float32 [tokens, top] (dweights may be None); load: int64
+    [experts + 1], or None without auxiliary losses; grad: logits_grad(...), written."""
+    n, d = _place(x)
+    _check(lib().mp_route_grad(ctypes.byref(x), _mask(mask, n, d), ctypes.byref(cfg),
+                               _array(ids, _I64, n * cfg.top, "ids", d),
+                               _array(dweights, _F32, n * cfg.top, "dweights", d),
+                               _array(load, _I64, x.vocab + 1, "load", d), float(balance_coef),
+                               float(z_coef), _grad_of(x, grad), _stream_of(stream, d)))
+
+
+def mp_route_bias_update(bias, load, speed, out=None, state=None, stream=None):
+    """bias: float32 [experts] or [layers, experts]; load: int64 [..., layers, experts + 1], of any
+    number of micro-batches; out: like bias (None: the bias is replaced); state: skipped with its
+    step."""
+    out = bias if out is None else out
+    experts = bias.shape[-1]
+    n = bias.numel()
+    layers = n // experts if experts else 0
+    if load.dim() < bias.dim() or load.shape[-1] != experts + 1 or (
+            bias.dim() > 1 and load.shape[-2] != layers) or bias.dim() > 2:
+        raise ValueError("load must be [..., layers, experts + 1] for a bias of [layers, experts]")
+    if out.shape != bias.shape:
+        raise ValueError("out must have the bias's shape")
+    total, d = load.numel(), bias.device
+    loads = total // (layers * (experts + 1)) if layers else 1
+    if bias.dim() == 1:
+        layers = 1
+    _check(lib().mp_route_bias_update(layers, experts, _array(bias, _F32, n, "bias"), loads,
+                                      _array(load, _I64, total, "load", d), float(speed),
+                                      _array(out, _F32, n, "out", d), state,
+                                      _stream_of(stream, d if bias.is_cuda else None)))
 
 
 # --- convenience ---------------------------------------------------------------

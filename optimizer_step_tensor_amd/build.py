@@ -7,7 +7,8 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libmpstep.so")
 SOURCES = [os.path.join(HERE, "csrc", f) for f in ("api.hip", "kernels.hip", "losses_api.hip",
                                                    "losses.hip", "scores_api.hip",
-                                                   "scores.hip")]
+                                                   "scores.hip", "routing_api.hip",
+                                                   "routing.hip")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 # -ffp-contract=off: no fusing of a*b+c, every operation rounds as written.

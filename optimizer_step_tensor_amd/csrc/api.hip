@@ -12,6 +12,7 @@
 
 #include "internal.h"
 #include "losses.h"
+#include "routing.h"
 
 using mpk::Chunk;
 using mpk::DevState;
@@ -427,6 +428,13 @@ mp_status set_error(mp_status st, const char* fmt, ...)
 mp_status set_ok()
 {
     return ok();
+}
+
+mp_status state_found_inf(const mp_state* state, const int32_t** flag)
+{
+    mp_status st = check_device(state->device, "the state");
+    if (st == MP_OK) *flag = &state->d->s.found_inf;
+    return st;
 }
 
 }  // namespace mpk
