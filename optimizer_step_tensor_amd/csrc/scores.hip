@@ -47,12 +47,13 @@ struct Share {
     float s = 0.0f, c = 0.0f;
 };
 
+// N elements; returns their maximum.
 template <int N>
-__device__ __forceinline__ void add(Share& a, const float (&f)[N], float k)
+__device__ __forceinline__ float add(Share& a, const float (&f)[N], float k)
 {
-    float g = a.m;
+    float g = f[0];
 #pragma unroll
-    for (int i = 0; i < N; ++i) g = __builtin_fmaxf(g, f[i]);
+    for (int i = 1; i < N; ++i) g = __builtin_fmaxf(g, f[i]);
     if (g > a.m) {
         // an unlikely row's references may be limited; none is infinite, so nothing here is NaN
         const float r = __builtin_amdgcn_fmed3f(g * k, -kRefMost, kRefMost);
@@ -70,6 +71,7 @@ __device__ __forceinline__ void add(Share& a, const float (&f)[N], float k)
         a.s += e;
         a.c = __builtin_fmaf(e, __builtin_fmaxf(y, kGone), a.c);      // 0, not 0 * -inf
     }
+    return g;
 }
 
 // The same from differences to the row's maximum.
@@ -156,13 +158,18 @@ __device__ __forceinline__ RowStat stat_of(float m, double ref, double s, double
     return r;
 }
 
-// Entries in their order -- the larger logit first, of equal ones (-0 and 0) the lower id -- as whole
-// numbers, the first the largest.  0 comes after every entry.
-__device__ __forceinline__ uint64_t entry_key(float v, int id)
+// Floats in their order as whole numbers, -0 as 0.
+__device__ __forceinline__ uint32_t order_of(float v)
 {
     const uint32_t u = __float_as_uint(v + 0.0f);
-    const uint32_t up = u & 0x80000000u ? ~u : u | 0x80000000u;
-    return uint64_t(up) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(id));
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// Entries in their order -- the larger logit first, of equal ones the lower id -- as whole numbers, the
+// first the largest.  0 comes after every entry.
+__device__ __forceinline__ uint64_t entry_key(float v, int id)
+{
+    return uint64_t(order_of(v)) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(id));
 }
 
 __device__ __forceinline__ float key_value(uint64_t key)
@@ -176,38 +183,277 @@ __device__ __forceinline__ int key_id(uint64_t key)
     return static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(key));
 }
 
-// Calls f(value, id) for every element of a row, each in one lane.
-template <int DT, int THREADS, class F>
-__device__ __forceinline__ void each_element(const typename Fmt<DT>::T* x, const Span<DT>& sp, F f)
-{
-    constexpr int E = Fmt<DT>::E;
-    for (int i = threadIdx.x; i < sp.nvec; i += THREADS) {
-        const int at = sp.head + i * E;
-        float v[E];
-        unpack<DT>(load_vec<DT, false>(x + at), v);
-#pragma unroll
-        for (int j = 0; j < E; ++j) f(v[j], at + j);
+// What a workgroup goes over: the vectors [lo, hi) of a row, and the elements that lanes take singly.
+template <int DT>
+struct Piece {
+    const typename Fmt<DT>::T* x;      // the row
+    int head, lo, hi;
+    int one;                           // this lane's single element, or -1
+    float single;
+
+    __device__ __forceinline__ const typename Fmt<DT>::T* at(int vec) const
+    {
+        return x + head + int64_t(vec) * Fmt<DT>::E;
     }
-    const int one = sp.single(threadIdx.x);
-    if (one >= 0) f(widen<DT>(x[one]), one);
-}
+    // Calls f(value, id) for every element, each in one lane.
+    template <int THREADS, class F>
+    __device__ __forceinline__ void each(F f) const
+    {
+        constexpr int E = Fmt<DT>::E;
+        for (int i = lo + static_cast<int>(threadIdx.x); i < hi; i += THREADS) {
+            float v[E];
+            unpack<DT>(load_vec<DT, false>(at(i)), v);
+#pragma unroll
+            for (int j = 0; j < E; ++j) f(v[j], head + i * E + j);
+        }
+        if (one >= 0) f(single, one);
+    }
+};
+
+// The choice of the k largest of a piece.  While the sums are formed every lane leaves the maximum of
+// each pair of its vectors in a slot (the first 16 bits of its order: a bound that a comparison
+// may only find too high; several pairs share a slot in long rows).  The k-th largest of the lanes' own
+// maxima is a bound that at least k elements reach, and few more: k elements fall into different
+// lanes mostly.  So the slots that reach it name the few vectors that are read again, and what of them
+// reaches it is ranked by counting, as (logit, id) in one whole number.
+constexpr int kSlots = 32;
 
 template <int THREADS>
-__device__ __forceinline__ uint64_t block_max(uint64_t v)
+struct Lists {
+    static constexpr int kKeys = 8 * THREADS, kHits = 4 * THREADS;
+    union {
+        uint16_t slot[kSlots * THREADS];
+        uint64_t key[kKeys];
+    };
+    uint32_t hit[kHits];
+    uint32_t lane_max[THREADS];
+    int hits, keys, above, bin;
+};
+
+template <int THREADS>
+__device__ __forceinline__ void put_key(Lists<THREADS>& l, uint64_t key)
 {
-    __shared__ uint64_t part[THREADS / kWave];
+    const int i = atomicAdd(&l.keys, 1);
+    if (i < Lists<THREADS>::kKeys) l.key[i] = key;
+}
+
+// Shares of a piece's vectors, and with TOP the slots; `per` pairs to a slot.
+template <int DT, int THREADS, bool TOP, bool NT>
+__device__ __forceinline__ void piece_sums(Share& share, const Piece<DT>& p, float k, Lists<THREADS>& l, int per)
+{
+    constexpr int E = Fmt<DT>::E, U = 4;
+    const int tid = threadIdx.x;
+    int slot = tid, left = per;
+    auto pair = [&](u32x4 a, u32x4 b, bool in_a, bool in_b) {
+        float f[2][E];
+        unpack<DT>(a, f[0]);
+        unpack<DT>(b, f[1]);
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            if (!in_a) f[0][j] = -__builtin_inff();
+            if (!in_b) f[1][j] = -__builtin_inff();
+        }
+        const float g = add(share, reinterpret_cast<const float(&)[2 * E]>(f), k);
+        if constexpr (TOP) {
+            uint16_t o = static_cast<uint16_t>(order_of(g) >> 16);
+            if (left != per) o = max(o, l.slot[slot]);
+            l.slot[slot] = o;
+            if (--left == 0) {
+                left = per;
+                slot += THREADS;
+            }
+        }
+    };
+    int base = p.lo;
+    for (; base + U * THREADS <= p.hi; base += U * THREADS) {
+        u32x4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = load_vec<DT, NT>(p.at(base + u * THREADS + tid));
+#pragma unroll
+        for (int u = 0; u < U; u += 2) pair(v[u], v[u + 1], true, true);
+    }
+    for (; base < p.hi; base += 2 * THREADS) {
+        const int i = base + tid, j = i + THREADS;
+        const u32x4 a = load_vec<DT, NT>(p.at(min(i, p.hi - 1)));
+        const u32x4 b = load_vec<DT, NT>(p.at(min(j, p.hi - 1)));
+        pair(a, b, i < p.hi, j < p.hi);
+    }
+}
+
+// A bound on the order that at least k of the workgroup's lane maxima reach and not many more: found
+// bit by bit, by every wave alike.
+template <int THREADS>
+__device__ __forceinline__ uint32_t lane_bound(const Lists<THREADS>& l, int k)
+{
+    constexpr int N = THREADS / kWave;
+    uint32_t v[N], lo = ~0u, hi = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        v[i] = l.lane_max[i * kWave + threadIdx.x % kWave];
+        lo = min(lo, v[i]);
+        hi = max(hi, v[i]);
+    }
 #pragma unroll
     for (int d = 1; d < kWave; d *= 2) {
-        const uint64_t o = __shfl_xor(v, d);
-        v = o > v ? o : v;
+        lo = min(lo, static_cast<uint32_t>(__shfl_xor(static_cast<int>(lo), d)));
+        hi = max(hi, static_cast<uint32_t>(__shfl_xor(static_cast<int>(hi), d)));
+    }
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    hi = __builtin_amdgcn_readfirstlane(hi);
+    int bit = 31 - __builtin_clz((lo ^ hi) | 1);
+    uint32_t bound = hi >> bit >> 1 << bit << 1;              // what all have in common
+    for (; bit >= 0; --bit) {
+        const uint32_t trial = bound | 1u << bit;
+        int c = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) c += __builtin_popcountll(__builtin_amdgcn_ballot_w64(v[i] >= trial));
+        if (c < k) continue;
+        bound = trial;
+        if (c <= k + k / 4 + 2) break;
+    }
+    return max(bound, 0x00800000u);                           // -inf is no entry
+}
+
+// Where the bound leaves too many (nearly equal rows, and rows made for it): the exact bound of the k
+// largest keys, eight bits at a time from histograms, each a pass over the piece, until few enough
+// reach it.
+template <int DT, int THREADS>
+__device__ __forceinline__ void choose_by_passes(const Piece<DT>& p, int k, Lists<THREADS>& l)
+{
+    uint32_t* const count = l.hit;
+    uint64_t prefix = 0, bound;
+    int before = 0;
+    for (int shift = 56;; shift -= 8) {
+        __syncthreads();
+        for (int i = threadIdx.x; i < 256; i += THREADS) count[i] = 0;
+        __syncthreads();
+        p.template each<THREADS>([&](float v, int id) {
+            const uint64_t key = entry_key(v, id);
+            const bool in = v > -__builtin_inff() && (shift == 56 || key >> shift >> 8 == prefix);
+            const int bin = in ? static_cast<int>(key >> shift & 255) : -1;
+            // all of a wave in one bin is the common case here
+            const int first = __builtin_amdgcn_readfirstlane(bin);
+            const uint64_t alike = __builtin_amdgcn_ballot_w64(bin == first);
+            if (bin == first) {
+                if (in && threadIdx.x % kWave == __builtin_ctzll(alike))
+                    atomicAdd(&count[bin], static_cast<uint32_t>(__builtin_popcountll(alike)));
+            } else if (in) {
+                atomicAdd(&count[bin], 1u);
+            }
+        });
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            int c = before, b = 255;
+            for (; b > 0; --b) {
+                if (c + static_cast<int>(count[b]) >= k) break;
+                c += static_cast<int>(count[b]);
+            }
+            l.above = c;
+            l.bin = b;
+        }
+        __syncthreads();
+        before = l.above;
+        prefix = prefix << 8 | static_cast<uint64_t>(l.bin);
+        if (shift == 0 || before + static_cast<int>(count[l.bin]) <= Lists<THREADS>::kKeys) {
+            bound = prefix << shift;
+            break;
+        }
     }
     __syncthreads();
-    if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = v;
+    if (threadIdx.x == 0) l.keys = 0;
     __syncthreads();
-    v = part[0];
+    p.template each<THREADS>([&](float v, int id) {
+        const uint64_t key = entry_key(v, id);
+        if (v > -__builtin_inff() && key >= bound) put_key(l, key);
+    });
+    __syncthreads();
+}
+
+// Calls emit(rank, key) for the k largest of l.key[0 .. n), the largest first, and emit(rank, 0) for
+// the ranks that are left.
+template <int THREADS, class F>
+__device__ __forceinline__ void emit_ranked(const Lists<THREADS>& l, int n, int k, F emit)
+{
+    for (int i = threadIdx.x; i < n; i += THREADS) {
+        const uint64_t own = l.key[i];
+        int rank = 0;
+        for (int j = 0; j < n; ++j) rank += l.key[j] > own;
+        if (rank < k) emit(rank, own);
+    }
+    for (int i = n + static_cast<int>(threadIdx.x); i < k; i += THREADS) emit(i, uint64_t(0));
+}
+
+template <int DT, int THREADS, class F>
+__device__ __forceinline__ void choose(const Piece<DT>& p, float lane_max, int per, int k, Lists<THREADS>& l,
+                                       F emit)
+{
+    constexpr int E = Fmt<DT>::E;
+    const int tid = threadIdx.x;
+    l.lane_max[tid] = order_of(lane_max);
+    if (tid == 0) l.hits = l.keys = 0;
+    __syncthreads();
+    const uint32_t bound = lane_bound(l, k);
+    const int pairs = (p.hi - p.lo + 2 * THREADS - 1) / (2 * THREADS);
+    const int slots = (pairs + per - 1) / per;
+    for (int i = 0; i < slots; ++i)
+        if (l.slot[i * THREADS + tid] >= bound >> 16) {
+            const int at = atomicAdd(&l.hits, 1);
+            if (at < Lists<THREADS>::kHits) l.hit[at] = i * THREADS + tid;
+        }
+    __syncthreads();                          // from here on keys take the slots' place
+    const int hits = l.hits;
+    if (hits <= Lists<THREADS>::kHits) {
+        const int each = 2 * per;
+        for (int i = tid; i < hits * each; i += THREADS) {
+            const int h = static_cast<int>(l.hit[i / each]);
+            const int vec = p.lo + (h / THREADS * each + i % each) * THREADS + h % THREADS;
+            if (vec >= p.hi) continue;
+            float v[E];
+            unpack<DT>(load_vec<DT, false>(p.at(vec)), v);
 #pragma unroll
-    for (int i = 1; i < THREADS / kWave; ++i) v = part[i] > v ? part[i] : v;
-    return v;
+            for (int j = 0; j < E; ++j)
+                if (order_of(v[j]) >= bound) put_key(l, entry_key(v[j], p.head + vec * E + j));
+        }
+        if (p.one >= 0 && order_of(p.single) >= bound) put_key(l, entry_key(p.single, p.one));
+        __syncthreads();
+    }
+    if (hits > Lists<THREADS>::kHits || l.keys > Lists<THREADS>::kKeys) choose_by_passes(p, k, l);
+    emit_ranked(l, l.keys, k, emit);
+}
+
+// The sums of a piece, in all lanes: relative to 2^ref.
+struct PieceStat {
+    double ref, s, c;
+    float m;
+};
+
+template <int DT, int THREADS, bool TOP>
+__device__ __forceinline__ PieceStat piece_stat(const Piece<DT>& p, float k, bool stream, int per,
+                                                Lists<THREADS>& l, JoinSpace<THREADS>& space, float& lane_max)
+{
+    Share share;
+    if (stream) piece_sums<DT, THREADS, TOP, true>(share, p, k, l, per);
+    else piece_sums<DT, THREADS, TOP, false>(share, p, k, l, per);
+    if (p.one >= 0) {
+        const float f[1] = {p.single};
+        add(share, f, k);
+    }
+    lane_max = share.m;
+    PieceStat r;
+    float ref;
+    join<THREADS>(share, space, r.m, ref, r.s, r.c);
+    r.ref = static_cast<double>(ref);
+    if (!(__builtin_fabsf(r.m * k) < kRowMost)) {
+        share = Share{};
+        share.m = r.m;
+        p.template each<THREADS>([&](float v, int) {
+            const float f[1] = {v};
+            add_to(share, f, k);
+        });
+        join<THREADS>(share, space, r.m, ref, r.s, r.c);
+        r.ref = static_cast<double>(r.m) * static_cast<double>(k);
+    }
+    return r;
 }
 
 __device__ __forceinline__ void write_entry(const ScoreArgs& a, int64_t at, uint64_t key, const RowStat& r)
@@ -244,12 +490,13 @@ __device__ __forceinline__ void write_off(const ScoreArgs& a, int64_t row)
     for (int e = threadIdx.x; e < a.top; e += blockDim.x) write_entry(a, row * a.top + e, 0, RowStat{});
 }
 
-// One row per workgroup, in one pass for the sums, then one for each entry.
-template <int DT, int THREADS>
-__global__ __launch_bounds__(THREADS) void k_scores(ScoreArgs a)
+// One row per workgroup.
+template <int DT, int THREADS, bool TOP>
+__global__ __launch_bounds__(THREADS) void k_scores(ScoreArgs a, int per)
 {
     using T = typename Fmt<DT>::T;
     __shared__ JoinSpace<THREADS> space;
+    __shared__ Lists<TOP ? THREADS : 1> lists;
     const int64_t row = blockIdx.x;
     const int n = a.x.vocab;
     const T* x = static_cast<const T*>(a.x.x) + row * a.x.stride;
@@ -257,37 +504,124 @@ __global__ __launch_bounds__(THREADS) void k_scores(ScoreArgs a)
     if (target < 0) return write_off(a, row);
     const RowScale k = scale_of(a.x);
     const Span<DT> sp(x, n);
-    Share share;
-    each_element<DT, THREADS>(x, sp, [&](float v, int) {
-        const float f[1] = {v};
-        add(share, f, k.k);
-    });
-    float m, ref;
-    double s, c;
-    join<THREADS>(share, space, m, ref, s, c);
-    double exact_ref = static_cast<double>(ref);
-    if (!(__builtin_fabsf(m * k.k) < kRowMost)) {
-        share = Share{};
-        share.m = m;
-        each_element<DT, THREADS>(x, sp, [&](float v, int) {
-            const float f[1] = {v};
-            add_to(share, f, k.k);
-        });
-        join<THREADS>(share, space, m, ref, s, c);
-        exact_ref = static_cast<double>(m) * static_cast<double>(k.k);
+    Piece<DT> p;
+    p.x = x;
+    p.head = sp.head;
+    p.lo = 0;
+    p.hi = sp.nvec;
+    p.one = sp.single(threadIdx.x);
+    p.single = p.one >= 0 ? widen<DT>(x[p.one]) : 0.0f;
+    const float xt = target < n ? widen<DT>(x[target]) : 0.0f;
+    float lane_max;
+    auto& l = reinterpret_cast<Lists<THREADS>&>(lists);
+    const PieceStat st = piece_stat<DT, THREADS, TOP>(p, k.k, a.x.stream, per, l, space, lane_max);
+    const RowStat r = stat_of(st.m, st.ref, st.s, st.c, k);
+    if (threadIdx.x == 0) write_row(a, row, target, xt, r);
+    if constexpr (TOP) {
+        auto emit = [&](int rank, uint64_t key) { write_entry(a, row * a.top + rank, key, r); };
+        if (r.ln_s == r.ln_s) {
+            choose<DT, THREADS>(p, lane_max, per, a.top, l, emit);
+        } else {
+            for (int e = threadIdx.x; e < a.top; e += THREADS) emit(e, 0);
+        }
     }
-    const RowStat r = stat_of(m, exact_ref, s, c, k);
-    if (threadIdx.x == 0) write_row(a, row, target, target < n ? widen<DT>(x[target]) : 0.0f, r);
-    uint64_t last = ~uint64_t(0);
-    for (int e = 0; e < a.top; ++e) {
-        uint64_t best = 0;
-        if (last != 0 && r.ln_s == r.ln_s)
-            each_element<DT, THREADS>(x, sp, [&](float v, int id) {
-                const uint64_t key = entry_key(v, id);
-                if (v > -__builtin_inff() && key < last && key > best) best = key;
-            });
-        last = block_max<THREADS>(best);
-        if (threadIdx.x == 0) write_entry(a, row * a.top + e, last, r);
+}
+
+// Few rows, less than the chip has room for: a row is cut into parts, one workgroup each, that leave
+// their sums and their own k largest in the workspace; then one workgroup a row joins them.
+constexpr int kPartThreads = 256;
+constexpr int kMaxParts = kWave;
+
+struct ScoreParts {
+    PieceStat* stat;         // rows x parts
+    uint64_t* key;           // rows x parts x top
+    int parts, vecs;         // per row; vectors of a part
+};
+
+template <int DT, bool TOP>
+__global__ __launch_bounds__(kPartThreads) void k_score_parts(ScoreArgs a, ScoreParts w, int per)
+{
+    using T = typename Fmt<DT>::T;
+    __shared__ JoinSpace<kPartThreads> space;
+    __shared__ Lists<TOP ? kPartThreads : 1> lists;
+    const unsigned parts = static_cast<unsigned>(w.parts);
+    const int64_t row = blockIdx.x / parts;
+    const int part = static_cast<int>(blockIdx.x % parts);
+    const T* x = static_cast<const T*>(a.x.x) + row * a.x.stride;
+    if (a.targets != nullptr && read_table(a.targets + row) < 0) return;
+    const RowScale k = scale_of(a.x);
+    const Span<DT> sp(x, a.x.vocab);
+    Piece<DT> p;
+    p.x = x;
+    p.head = sp.head;
+    p.lo = min(part * w.vecs, sp.nvec);
+    p.hi = min(p.lo + w.vecs, sp.nvec);
+    p.one = part == 0 ? sp.single(threadIdx.x) : -1;
+    p.single = p.one >= 0 ? widen<DT>(x[p.one]) : 0.0f;
+    float lane_max;
+    auto& l = reinterpret_cast<Lists<kPartThreads>&>(lists);
+    const PieceStat st = piece_stat<DT, kPartThreads, TOP>(p, k.k, false, per, l, space, lane_max);
+    if (threadIdx.x == 0) w.stat[blockIdx.x] = st;
+    if constexpr (TOP)
+        choose<DT, kPartThreads>(p, lane_max, per, a.top, l, [&](int rank, uint64_t key) {
+            w.key[int64_t(blockIdx.x) * a.top + rank] = key;
+        });
+}
+
+template <int DT, bool TOP>
+__global__ __launch_bounds__(kPartThreads) void k_score_join(ScoreArgs a, ScoreParts w)
+{
+    using T = typename Fmt<DT>::T;
+    __shared__ Lists<TOP ? kPartThreads : 1> lists;
+    const int64_t row = blockIdx.x;
+    const int n = a.x.vocab, tid = threadIdx.x, lane = tid % kWave;
+    const T* x = static_cast<const T*>(a.x.x) + row * a.x.stride;
+    const int64_t target = a.targets != nullptr ? read_table(a.targets + row) : 0;
+    if (target < 0) return write_off(a, row);
+    const RowScale k = scale_of(a.x);
+    const float xt = target < n ? widen<DT>(x[target]) : 0.0f;
+    PieceStat st{-__builtin_inf(), 0.0, 0.0, -FLT_MAX};
+    if (lane < w.parts) st = w.stat[row * w.parts + lane];
+    const float m = lanes_max<kWave>(st.m);
+    // a part without any element in reach has no say in the reference; a NaN's is kept
+    double ref = st.s != 0.0 ? st.ref : -__builtin_inf();
+    const double own = st.ref;
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) {
+        const double o = __shfl_xor(ref, d);
+        ref = o > ref ? o : ref;
+    }
+    const double d = st.s != 0.0 ? own - ref : 0.0;
+    const double down = static_cast<double>(exp2_hw(static_cast<float>(d)));
+    const double c = lanes_sum<kWave>(down == 0.0 ? 0.0 : (st.c + st.s * d) * down);
+    const double s = lanes_sum<kWave>(st.s * down);
+    const RowStat r = stat_of(m, ref, s, c, k);
+    if (tid == 0) write_row(a, row, target, xt, r);
+    if constexpr (TOP) {
+        auto& l = reinterpret_cast<Lists<kPartThreads>&>(lists);
+        const uint64_t* key = w.key + row * w.parts * a.top;
+        if (r.ln_s != r.ln_s) {
+            for (int e = tid; e < a.top; e += kPartThreads) write_entry(a, row * a.top + e, 0, r);
+            return;
+        }
+        // of P sorted lists the k / P-th entries: at least k entries reach the smallest of them
+        const int deep = (a.top + w.parts - 1) / w.parts - 1;
+        uint64_t bound = lane < w.parts ? key[lane * a.top + deep] : ~uint64_t(0);
+#pragma unroll
+        for (int e = 1; e < kWave; e *= 2) {
+            const uint64_t o = __shfl_xor(bound, e);
+            bound = o < bound ? o : bound;
+        }
+        if (bound == 0) bound = 1;                     // an empty place is no entry
+        if (tid == 0) l.keys = 0;
+        __syncthreads();
+        for (int i = tid; i < w.parts * a.top; i += kPartThreads) {
+            const uint64_t v = key[i];
+            if (v >= bound) put_key(l, v);             // at most parts * top <= kKeys
+        }
+        __syncthreads();
+        emit_ranked(l, l.keys, a.top,
+                    [&](int rank, uint64_t v) { write_entry(a, row * a.top + rank, v, r); });
     }
 }
 
@@ -370,10 +704,69 @@ __global__ __launch_bounds__(kGradThreads) void k_score_grad(ScoreGradArgs a, in
     }
 }
 
-template <int DT>
-void scores_dt(const ScoreArgs& a, hipStream_t s)
+// Pairs that share a slot where `vecs` vectors are dealt to `threads` lanes.
+int pairs_per_slot(int vecs, int threads)
 {
-    k_scores<DT, 256><<<static_cast<unsigned>(a.x.rows), 256, 0, s>>>(a);
+    const int pairs = (vecs + 2 * threads - 1) / (2 * threads);
+    const int per = (pairs + kSlots - 1) / kSlots;
+    return per > 0 ? per : 1;
+}
+
+template <int DT, int THREADS>
+void whole_rows(const ScoreArgs& a, hipStream_t s)
+{
+    const unsigned rows = static_cast<unsigned>(a.x.rows);
+    const int per = pairs_per_slot(a.x.vocab / Fmt<DT>::E, THREADS);
+    if (a.top > 0) k_scores<DT, THREADS, true><<<rows, THREADS, 0, s>>>(a, per);
+    else k_scores<DT, THREADS, false><<<rows, THREADS, 0, s>>>(a, per);
+}
+
+constexpr int kSplitRows = 128;
+constexpr int kSplitVocab = 16 * 1024;
+
+// Split the rows over several workgroups?  Fills `w` in the workspace if so.
+template <int DT>
+bool split(const ScoreArgs& a, ScoreParts* w)
+{
+    if (a.workspace == nullptr || a.x.rows > kSplitRows || a.x.vocab < kSplitVocab) return false;
+    const int nvec = a.x.vocab / Fmt<DT>::E;
+    int parts = 512 / a.x.rows;
+    if (parts > kMaxParts) parts = kMaxParts;
+    if (a.top > 0 && parts > Lists<kPartThreads>::kKeys / a.top) parts = Lists<kPartThreads>::kKeys / a.top;
+    const int most = (nvec + 2 * kPartThreads - 1) / (2 * kPartThreads);
+    if (parts > most) parts = most;
+    if (parts < 2) return false;
+    w->vecs = (nvec + parts - 1) / parts;
+    w->parts = (nvec + w->vecs - 1) / w->vecs;
+    const int64_t pieces = int64_t(a.x.rows) * w->parts;
+    const size_t stats = sizeof(PieceStat) * pieces;
+    if (stats + sizeof(uint64_t) * pieces * a.top > MP_SCORE_WORKSPACE_BYTES) return false;
+    w->stat = static_cast<PieceStat*>(a.workspace);
+    w->key = reinterpret_cast<uint64_t*>(static_cast<char*>(a.workspace) + stats);
+    return true;
+}
+
+template <int DT>
+void scores_dt(ScoreArgs a, hipStream_t s)
+{
+    a.x.stream = logits_bytes<DT>(a.x) > kCacheBytes;
+    ScoreParts w;
+    if (split<DT>(a, &w)) {
+        const unsigned rows = static_cast<unsigned>(a.x.rows), all = rows * static_cast<unsigned>(w.parts);
+        const int per = pairs_per_slot(w.vecs, kPartThreads);
+        if (a.top > 0) {
+            k_score_parts<DT, true><<<all, kPartThreads, 0, s>>>(a, w, per);
+            k_score_join<DT, true><<<rows, kPartThreads, 0, s>>>(a, w);
+        } else {
+            k_score_parts<DT, false><<<all, kPartThreads, 0, s>>>(a, w, per);
+            k_score_join<DT, false><<<rows, kPartThreads, 0, s>>>(a, w);
+        }
+        return;
+    }
+    const int nvec = a.x.vocab / Fmt<DT>::E;
+    // a bound from 64 lanes' maxima is one for at most 64 entries
+    if (nvec <= 64 * 8 && a.top <= 64) whole_rows<DT, 64>(a, s);
+    else whole_rows<DT, 256>(a, s);
 }
 
 template <int DT>
