@@ -3,10 +3,19 @@
 //
 // Experts are chosen by c_e = s_e + b_e, s = softmax(x) or sigmoid(x).  Two of a token's c are closer
 // than 2^-24 about once in 10^5 tokens, and fp32 arithmetic would then choose by its rounding
-// errors: c is formed in binary64, which runs at fp32's rate here.  A choice is made on c rounded to
-// 42 bits, with the expert's number in the last ten (`expert_key`), so that one maximum finds the
-// largest c and, of equal ones, the lowest number.
+// errors: c is formed in binary64, which runs at fp32's rate here, and rounded to 42 bits.  Without a bias
+// (and without sums of two scores) the order of c is that of the logits: no score is formed for the
+// choice then.
+//
+// A choice is made on keys, numbers that hold c (or the logit) and the expert, the lower the larger,
+// so that equal c fall to the lowest number and one maximum or minimum instruction is a whole step of
+// a sorting network: binary64 with the expert in the last ten bits, or, for 16-bit logits, whole numbers of
+// 32 bits.  L lanes share a token, each with P experts in chunks of eight neighbours; a lane sorts its
+// chunks and keeps the K best of them, and lanes join their lists in log2(L) steps.  Few lanes with many
+// experts do the least: a join costs the same however many lanes repeat it.
 #include <float.h>
+
+#include <type_traits>
 
 #include "rows.h"
 #include "routing.h"
@@ -14,23 +23,24 @@
 namespace mpk {
 namespace {
 
-// 2^y for -1100 <= y <= 1000: y's fraction by the exponential series (14 digits), its whole part as the
-// exponent.  (No table and no double-word steps: the library's exp takes twice the operations.)
+constexpr double kLog2E = 1.4426950408889634;
+
+// 2^y for -1100 <= y <= 1000: the fraction's power by Chebyshev interpolation of degree 10 on [-1/2, 1/2]
+// (relative error 3e-16), the whole part as the exponent.  The library's exp takes twice the operations.
 __device__ __forceinline__ double exp2_series(double y)
 {
     const double whole = __builtin_rint(y);
-    const double t = (y - whole) * 0.69314718055994531;        // |t| < 0.3466
-    double p = 1.0 / 39916800.0;                               // t^12 / 12! < 7e-15
-    p = __builtin_fma(p, t, 1.0 / 3628800.0);
-    p = __builtin_fma(p, t, 1.0 / 362880.0);
-    p = __builtin_fma(p, t, 1.0 / 40320.0);
-    p = __builtin_fma(p, t, 1.0 / 5040.0);
-    p = __builtin_fma(p, t, 1.0 / 720.0);
-    p = __builtin_fma(p, t, 1.0 / 120.0);
-    p = __builtin_fma(p, t, 1.0 / 24.0);
-    p = __builtin_fma(p, t, 1.0 / 6.0);
-    p = __builtin_fma(p, t, 0.5);
-    p = __builtin_fma(p, t, 1.0);
+    const double t = y - whole;
+    double p = 7.072585949269224e-09;
+    p = __builtin_fma(p, t, 1.0208690299958306e-07);
+    p = __builtin_fma(p, t, 1.321544258792169e-06);
+    p = __builtin_fma(p, t, 1.5252657260200837e-05);
+    p = __builtin_fma(p, t, 0.0001540353044173605);
+    p = __builtin_fma(p, t, 0.0013333558230164974);
+    p = __builtin_fma(p, t, 0.009618129107606888);
+    p = __builtin_fma(p, t, 0.05550410866444772);
+    p = __builtin_fma(p, t, 0.24022650695910097);
+    p = __builtin_fma(p, t, 0.69314718055995);
     p = __builtin_fma(p, t, 1.0);
     return __builtin_ldexp(p, static_cast<int>(whole));
 }
@@ -43,28 +53,30 @@ __device__ __forceinline__ double reciprocal(double d)
     return __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
 }
 
-constexpr double kLog2E = 1.4426950408889634;
-
-__device__ __forceinline__ double clamp_exponent(double y)
-{
-    return __builtin_fmin(__builtin_fmax(y, -1100.0), 1000.0);
-}
-
 __device__ __forceinline__ double sigmoid_of(float z)
 {
     const double y = static_cast<double>(z) * -kLog2E;
-    return y > 1000.0 ? 0.0 : reciprocal(1.0 + exp2_series(clamp_exponent(y)));
+    return y > 1000.0 ? 0.0 : reciprocal(1.0 + exp2_series(y < -1000.0 ? -1000.0 : y));
 }
 
 // exp(z - m), z <= m.
 __device__ __forceinline__ double share_to(float z, float m)
 {
-    return exp2_series(clamp_exponent((static_cast<double>(z) - static_cast<double>(m)) * kLog2E));
+    const double y = (static_cast<double>(z) - static_cast<double>(m)) * kLog2E;
+    return exp2_series(y < -1100.0 ? -1100.0 : y);
+}
+
+// The same in fp32, relative error 2^-24 (|z - m| + 2): x log2(e) with the constant in two parts.
+__device__ __forceinline__ float share_to_fast(float z, float m)
+{
+    constexpr float hi = 1.44269502162933349609375f, lo = 1.925963033500e-8f;
+    const float t = z - m;
+    return exp2_hw(__builtin_fmaf(t, lo, t * hi));
 }
 
 constexpr int kIdBits = 10;                              // MP_ROUTE_MAX_EXPERTS is 2^10
 constexpr uint64_t kIdMask = (1 << kIdBits) - 1;
-constexpr double kNoKey = -__builtin_inf();
+constexpr double kMost = 1e300;                          // so that no key is an infinity's or a NaN's
 
 // c (finite) as far as it counts: what is equal but for the rounding of sums is equal then.
 __device__ __forceinline__ uint64_t rounded(double c)
@@ -72,39 +84,131 @@ __device__ __forceinline__ uint64_t rounded(double c)
     return (__builtin_bit_cast(uint64_t, c + 0.0) + (kIdMask + 1) / 2) & ~kIdMask;       // -0 is 0
 }
 
-// A number that orders experts by c and then by lowest number.  Of a negative c the larger last bits
-// are the smaller number.
-__device__ __forceinline__ double expert_key(double c, int e)
+// Keys of type double or uint32_t.
+template <class Key>
+__device__ __forceinline__ Key no_key()
+{
+    if constexpr (std::is_same_v<Key, double>) return -__builtin_inf();
+    else return 0;
+}
+
+// Of a negative c the larger last bits are the smaller number.
+__device__ __forceinline__ double key_of(double c, int e)
 {
     const uint64_t u = rounded(c);
     return __builtin_bit_cast(double, u | (u >> 63 ? uint64_t(e) : kIdMask - uint64_t(e)));
 }
 
-__device__ __forceinline__ int key_expert(double key)
+// A 16-bit logit's order in the upper half (never 0: -inf has no key).
+template <int DT>
+__device__ __forceinline__ uint32_t key_of_logit(float z, int e)
 {
-    const uint64_t u = __builtin_bit_cast(uint64_t, key);
-    const int last = static_cast<int>(u & kIdMask);
-    return u >> 63 ? last : static_cast<int>(kIdMask) - last;
+    const float f = z + 0.0f;
+    const uint32_t h = DT == kBF16 ? __float_as_uint(f) >> 16
+                                   : __builtin_bit_cast(uint16_t, static_cast<_Float16>(f));
+    return (h & 0x8000u ? 0xFFFFu - h : h + 0x8000u) << 16 | (0xFFFFu - static_cast<uint32_t>(e));
 }
 
-__device__ __forceinline__ double max_of(double a, double b) { return a > b ? a : b; }
-
-template <int WIDTH, int D = 1>
-__device__ __forceinline__ double lanes_max_key(double v)
+template <class Key>
+__device__ __forceinline__ int key_expert(Key key)
 {
-    if constexpr (D < WIDTH) {
-        const uint64_t u = __builtin_bit_cast(uint64_t, v);
-        uint32_t a0, b0, a1, b1;
-        across<D>(static_cast<uint32_t>(u), a0, b0);
-        across<D>(static_cast<uint32_t>(u >> 32), a1, b1);
-        return lanes_max_key<WIDTH, 2 * D>(max_of(__builtin_bit_cast(double, uint64_t(a1) << 32 | a0),
-                                                  __builtin_bit_cast(double, uint64_t(b1) << 32 | b0)));
+    if constexpr (std::is_same_v<Key, double>) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, key);
+        const int last = static_cast<int>(u & kIdMask);
+        return u >> 63 ? last : static_cast<int>(kIdMask) - last;
+    } else {
+        return static_cast<int>(0xFFFFu - (key & 0xFFFFu));
     }
-    return v;
 }
 
-// A bound that no c reaches, so that a key has ten bits to spare of any.
-constexpr double kMost = 1e300;
+__device__ __forceinline__ double key_score(double key)
+{
+    return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, key) & ~kIdMask);
+}
+
+// Maximum and minimum: one instruction each.  (A binary64 one is written out: the compiler puts a
+// quieting of NaN before its own.  It depends on no unfinished result but through its operands.)
+__device__ __forceinline__ double max_key(double a, double b)
+{
+    double r;
+    asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+__device__ __forceinline__ double min_key(double a, double b)
+{
+    double r;
+    asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t max_key(uint32_t a, uint32_t b) { return max(a, b); }
+__device__ __forceinline__ uint32_t min_key(uint32_t a, uint32_t b) { return min(a, b); }
+
+template <class Key>
+__device__ __forceinline__ void order_pair(Key& a, Key& b)          // the larger first
+{
+    const Key hi = max_key(a, b);
+    b = min_key(a, b);
+    a = hi;
+}
+
+// Eight keys, the largest first, in 19 comparisons (Batcher's odd-even merge sort).
+template <class Key>
+__device__ __forceinline__ void sort8(Key (&k)[8])
+{
+    constexpr int pair[19][2] = {{0, 1}, {2, 3}, {4, 5}, {6, 7}, {0, 2}, {1, 3}, {4, 6}, {5, 7}, {1, 2}, {5, 6},
+                                 {0, 4}, {1, 5}, {2, 6}, {3, 7}, {2, 4}, {3, 5}, {1, 2}, {3, 4}, {5, 6}};
+#pragma unroll
+    for (int i = 0; i < 19; ++i) order_pair(k[pair[i][0]], k[pair[i][1]]);
+}
+
+// A bitonic list of K keys, the largest first.
+template <int K, class Key>
+__device__ __forceinline__ void sort_bitonic(Key (&k)[K])
+{
+#pragma unroll
+    for (int d = K / 2; d > 0; d /= 2)
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+            if (!(i & d)) order_pair(k[i], k[i + d]);
+}
+
+// Lane D away in groups that are alike below D (`across`).
+template <int D, class Key>
+__device__ __forceinline__ Key partner(Key v)
+{
+    // the row swaps give both values: which of them is the own one depends on the lane
+    if constexpr (std::is_same_v<Key, double>) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, v);
+        const uint32_t lo = partner<D>(static_cast<uint32_t>(u)), hi = partner<D>(static_cast<uint32_t>(u >> 32));
+        return __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
+    } else {
+        uint32_t a, b;
+        across<D>(v, a, b);
+        if constexpr (D >= 16) return threadIdx.x & D ? a : b;
+        else return b;
+    }
+}
+
+// The K best of two sorted lists, the other one a lane's D away.
+template <int D, int K, class Key>
+__device__ __forceinline__ void join_lists(Key (&k)[K])
+{
+    Key other[K];
+#pragma unroll
+    for (int i = 0; i < K; ++i) other[i] = partner<D>(k[i]);
+#pragma unroll
+    for (int i = 0; i < K; ++i) k[i] = max_key(k[i], other[K - 1 - i]);
+    sort_bitonic(k);
+}
+
+template <int L, int K, int D = 1, class Key>
+__device__ __forceinline__ void join_lanes(Key (&k)[K])
+{
+    if constexpr (D < L) {
+        join_lists<D>(k);
+        join_lanes<L, K, 2 * D>(k);
+    }
+}
 
 constexpr int kRouteThreads = 256;
 constexpr int kRouteWaves = kRouteThreads / kWave;
@@ -118,146 +222,301 @@ struct RouteSums {
     int groups;         // workgroups
 };
 
-// One wave per token, P experts a lane (expert lane + 64 i).
-template <int DT, int P, bool SIGMOID>
-__global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a, RouteSums w)
+// Eight neighbouring logits from element e of a row of n; -inf past its end.
+template <int DT>
+__device__ __forceinline__ void load8(const typename Fmt<DT>::T* x, int e, int n, float* z)
+{
+    constexpr int E = Fmt<DT>::E;
+    if (e + 8 <= n) {
+#pragma unroll
+        for (int i = 0; i < 8; i += E) {
+            float f[E];
+            unpack<DT>(load_vec<DT, false>(x + e + i), f);
+#pragma unroll
+            for (int j = 0; j < E; ++j) z[i + j] = f[j];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j] = e + j < n ? widen<DT>(x[e + j]) : -__builtin_inff();
+    }
+}
+
+// The waves of a workgroup share nothing but counts: what a wave writes to its own part of the shared
+// memory its lanes read back in order.
+__device__ __forceinline__ void wave_fence()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
+// Places for keys that the groups of a token are formed from: two for each chunk, or all experts where
+// the groups' borders are not the chunks'.
+__host__ __device__ __forceinline__ int group_keys(int n, int groups, int all)
+{
+    return groups == 1 ? 0 : n / groups % 8 == 0 ? all / 4 : all;
+}
+
+// L lanes per token, P experts a lane: expert (c L + lane) 8 + j is the lane's P's c 8 + j.
+template <int DT, int L, int P, int K, bool EXACT>
+__global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a, RouteSums w, int space_bytes)
 {
     using T = typename Fmt<DT>::T;
-    __shared__ double sum[kRouteWaves][MP_ROUTE_MAX_GROUPS];
-    __shared__ double c_of[kRouteWaves][P * kWave];
-    __shared__ int32_t count[P * kWave];
+    using Key = std::conditional_t<EXACT || DT == kFP32, double, uint32_t>;
+    constexpr int R = kWave / L, C = P / 8, N = L * P;         // tokens a wave, chunks a lane, experts
+    extern __shared__ __align__(16) char space[];       // a part for each wave
+    __shared__ int32_t count[N];
     __shared__ double square[kRouteWaves];
     __shared__ int32_t routed[kRouteWaves];
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const int sub = lane % L, slot = lane / L;
     const int n = a.x.vocab;
     const int width = n / a.groups;
-    const bool sums = w.share != nullptr;
+    const bool sums = w.share != nullptr, sigmoid = a.sigmoid != 0;
+    // this token's keys, the groups' and whether these are open
+    const int keys = group_keys(n, a.groups, N);
+    char* const own_space = space + wave * space_bytes;
+    Key* const mine = reinterpret_cast<Key*>(own_space) + slot * (keys + a.groups);
+    Key* const group_of = mine + keys;
+    uint8_t* const open_of = reinterpret_cast<uint8_t*>(reinterpret_cast<Key*>(own_space) + R * (keys + a.groups)) +
+                             slot * a.groups;
     double total[P] = {};
     double squares = 0.0;
     int tokens = 0;
     float bias[P] = {};
     if (sums) {
-        for (int e = threadIdx.x; e < P * kWave; e += kRouteThreads) count[e] = 0;
+        for (int e = threadIdx.x; e < N; e += kRouteThreads) count[e] = 0;
         __syncthreads();
     }
+    if constexpr (EXACT) {
+        if (a.bias != nullptr) {
 #pragma unroll
-    for (int i = 0; i < P; ++i)
-        if (a.bias != nullptr && lane + i * kWave < n) bias[i] = a.bias[lane + i * kWave];
-    for (int64_t row = int64_t(blockIdx.x) * kRouteWaves + wave; row < a.x.rows;
-         row += int64_t(gridDim.x) * kRouteWaves) {
-        const T* x = static_cast<const T*>(a.x.x) + row * a.x.stride;
-        float* weights = a.weights + row * a.top;
-        int64_t* ids = a.ids + row * a.top;
-        if (a.mask != nullptr && a.mask[row] == 0) {
-            if (lane < a.top) {
-                weights[lane] = 0.0f;
-                ids[lane] = -1;
+            for (int i = 0; i < P; ++i) {
+                const int e = (i / 8 * L + sub) * 8 + i % 8;
+                if (e < n) bias[i] = a.bias[e];
             }
-            continue;
         }
+    }
+    const int64_t step = int64_t(gridDim.x) * kRouteWaves * R;
+    for (int64_t first = (int64_t(blockIdx.x) * kRouteWaves + wave) * R; first < a.x.rows; first += step) {
+        const int64_t row = first + slot;
+        const bool live = row < a.x.rows && (a.mask == nullptr || a.mask[row] != 0);
+        const T* x = static_cast<const T*>(a.x.x) + row * a.x.stride;
         float z[P];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            if (live) load8<DT>(x, (c * L + sub) * 8, n, z + c * 8);
+            else
+                for (int j = 0; j < 8; ++j) z[c * 8 + j] = -__builtin_inff();
+        }
         bool bad = false;
         float m = -FLT_MAX;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const int e = lane + i * kWave;
-            z[i] = e < n ? widen<DT>(x[e]) : -__builtin_inff();
-            bad |= z[i] != z[i] || (!SIGMOID && z[i] == __builtin_inff());
+            bad |= z[i] != z[i];
             m = __builtin_fmaxf(m, z[i]);
         }
-        m = lanes_max<kWave>(m);
-        double s[P];
+        m = lanes_max<L>(m);
+        // +inf is the largest then; nothing but -inf leaves the sum 0
+        bad = lanes_max<L>(bad ? 1.0f : 0.0f) > 0.0f || (!sigmoid && m == __builtin_inff());
+
+        // the scores, where the choice or a sum over the tokens wants all of them
+        Key key[P];
         double all = 0.0;
+        float s[P];                     // shares of a softmax, scores of a sigmoid: for the sums
+        double part = 0.0;
+        if constexpr (EXACT) {
+            double c[P];
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            // -inf: no expert there, a share of 0
-            s[i] = z[i] == -__builtin_inff() ? 0.0 : SIGMOID ? sigmoid_of(z[i]) : share_to(z[i], m);
-            all += s[i];
-        }
-        all = lanes_sum<kWave>(all);
-        if (__builtin_amdgcn_ballot_w64(bad) != 0 || (!SIGMOID && !(all > 0.0))) {
-            if (lane < a.top) {                      // no distribution
-                weights[lane] = __builtin_nanf("");
-                ids[lane] = -1;
+            for (int i = 0; i < P; ++i) {
+                c[i] = sigmoid ? sigmoid_of(z[i]) : share_to(z[i], m);          // -inf: 0
+                all += c[i];
             }
-            continue;
-        }
-        const double part = all > 0.0 ? 1.0 / all : 0.0;
-        double key[P];
+            all = lanes_sum<L>(all);
+            part = all > 0.0 ? 1.0 / all : 0.0;
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            if (!SIGMOID) s[i] *= part;
-            double c = s[i] + static_cast<double>(bias[i]);
-            const bool in = z[i] > -__builtin_inff() && c > -__builtin_inf();
-            c = __builtin_fmin(c, kMost);
-            key[i] = in ? expert_key(c, lane + i * kWave) : kNoKey;
-            if (a.groups > 1) c_of[wave][lane + i * kWave] = in ? c : -__builtin_inf();
+            for (int i = 0; i < P; ++i) {
+                if (!sigmoid) c[i] *= part;
+                s[i] = static_cast<float>(c[i]);
+                double v = c[i] + static_cast<double>(bias[i]);
+                const bool in = z[i] > -__builtin_inff() && v > -__builtin_inf();
+                v = v < kMost ? v : kMost;
+                key[i] = in ? key_of(v, (i / 8 * L + sub) * 8 + i % 8) : no_key<Key>();
+            }
+        } else {
+            if (sums || !(sigmoid || a.renormalise)) {
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    if (sigmoid) {
+                        const float u = exp2_hw(-__builtin_fabsf(z[i]) * static_cast<float>(kLog2E));
+                        s[i] = (z[i] >= 0.0f ? 1.0f : u) * __builtin_amdgcn_rcpf(1.0f + u);
+                    } else {
+                        s[i] = share_to_fast(z[i], m);
+                    }
+                    all += static_cast<double>(s[i]);
+                }
+                all = lanes_sum<L>(all);
+                part = all > 0.0 ? 1.0 / all : 0.0;
+            }
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const int e = (i / 8 * L + sub) * 8 + i % 8;
+                if constexpr (DT == kFP32) key[i] = key_of(static_cast<double>(z[i]), e);
+                else key[i] = key_of_logit<DT>(z[i], e);
+                if (!(z[i] > -__builtin_inff())) key[i] = no_key<Key>();
+            }
+            if constexpr (DT == kFP32) {
+                if (sigmoid && m == __builtin_inff()) {         // its key would be a NaN's
+#pragma unroll
+                    for (int i = 0; i < P; ++i)
+                        if (z[i] == __builtin_inff()) key[i] = key_of(kMost, (i / 8 * L + sub) * 8 + i % 8);
+                }
+            }
         }
+        const bool none = !live || bad;
+
+        // groups whose borders are not the chunks': their experts one by one
+        const bool by_chunk = width % 8 == 0;
         if (a.groups > 1) {
-            // a wave's accesses to its own shared memory are in order
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            double mine = -__builtin_inf();
-            if (lane < a.groups) {
-                double first = -__builtin_inf(), second = -__builtin_inf();
-                for (int i = 0; i < width; ++i) {
-                    const double c = c_of[wave][lane * width + i];
-                    second = max_of(second, c < first ? c : first);
-                    first = max_of(first, c);
-                }
-                if (first > -__builtin_inf())
-                    mine = __builtin_bit_cast(
-                        double, rounded(first + (a.group_best == 2 && second > -__builtin_inf() ? second : 0.0)));
-                sum[wave][lane] = mine;
+            wave_fence();
+            if (!by_chunk) {
+#pragma unroll
+                for (int i = 0; i < P; ++i) mine[(i / 8 * L + sub) * 8 + i % 8] = key[i];
             }
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            int before = 0;
-            if (lane < a.groups)
-                for (int g = 0; g < a.groups; ++g) {
-                    const double o = sum[wave][g];
-                    before += o > mine || (o == mine && g < lane);
+        }
+        Key list[K];
+#pragma unroll
+        for (int i = 0; i < K; ++i) list[i] = no_key<Key>();
+        auto open_groups = [&](int per, int stride) {
+            // group g: `per` places of `stride` keys, the first two of each place its largest
+            wave_fence();
+            for (int g = sub; g < a.groups; g += L) {
+                Key best = no_key<Key>(), next = no_key<Key>();
+                for (int i = 0; i < per; ++i) {
+                    const Key u = mine[(g * per + i) * stride];
+                    next = max_key(next, min_key(best, u));
+                    best = max_key(best, u);
+                    if (stride > 1) next = max_key(next, mine[(g * per + i) * stride + 1]);
                 }
-            const uint64_t kept = __builtin_amdgcn_ballot_w64(lane < a.groups && before < a.top_groups);
+                if constexpr (EXACT) {
+                    if (a.group_best == 2 && best > no_key<Key>())
+                        best = __builtin_bit_cast(
+                            double, rounded(key_score(best) + (next > no_key<Key>() ? key_score(next) : 0.0)));
+                }
+                group_of[g] = best;
+            }
+            wave_fence();
+            for (int g = sub; g < a.groups; g += L) {
+                const Key own = group_of[g];
+                int before = 0;
+                for (int o = 0; o < a.groups; ++o) {
+                    const Key other = group_of[o];
+                    before += other > own || (other == own && o < g);
+                }
+                open_of[g] = before < a.top_groups;
+            }
+            wave_fence();
+        };
+        if (a.groups > 1 && !by_chunk) {
+            open_groups(width, 1);
 #pragma unroll
-            for (int i = 0; i < P; ++i)
-                if (!(kept >> ((lane + i * kWave) / width % 64) & 1)) key[i] = kNoKey;
+            for (int i = 0; i < P; ++i) {
+                const int e = (i / 8 * L + sub) * 8 + i % 8;
+                if (e < n && !open_of[e / width]) key[i] = no_key<Key>();
+            }
         }
-        double chosen = kNoKey;          // lane i: the i-th expert
-        for (int i = 0; i < a.top; ++i) {
-            double best = key[0];
 #pragma unroll
-            for (int j = 1; j < P; ++j) best = max_of(best, key[j]);
-            best = lanes_max_key<kWave>(best);
-            if (lane == i) chosen = best;
+        for (int c = 0; c < C; ++c) sort8(reinterpret_cast<Key(&)[8]>(key[c * 8]));
+        if (a.groups > 1 && by_chunk) {
 #pragma unroll
-            for (int j = 0; j < P; ++j)
-                if (key[j] == best) key[j] = kNoKey;
-        }
-        const bool there = chosen > kNoKey;
-        const int e = there ? key_expert(chosen) : 0;
-        double ws = 0.0;
-        if (there) {
-            const float ze = widen<DT>(x[e]);
-            ws = SIGMOID ? sigmoid_of(ze) : share_to(ze, m) * part;
-        }
-        const double d = lanes_sum<kWave>(ws) + kTiny;
-        if (lane < a.top) {
-            weights[lane] = static_cast<float>((a.renormalise ? ws / d : ws) * static_cast<double>(a.scale));
-            ids[lane] = there ? e : -1;
-            if (sums && there) atomicAdd(&count[e], 1);
-        }
-        if (sums && __builtin_amdgcn_ballot_w64(there) != 0) {
-            ++tokens;
+            for (int c = 0; c < C; ++c) {
+                mine[(c * L + sub) * 2] = key[c * 8];
+                mine[(c * L + sub) * 2 + 1] = key[c * 8 + 1];
+            }
+            open_groups(width / 8, 2);
 #pragma unroll
-            for (int i = 0; i < P; ++i) total[i] += SIGMOID ? s[i] * part : s[i];
-            if (!SIGMOID) {
-                const double lse = static_cast<double>(m) + log_sum(all);
-                squares += lse * lse;
+            for (int c = 0; c < C; ++c) {
+                const int e = (c * L + sub) * 8;
+                if (e < n && !open_of[e / width]) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) key[c * 8 + j] = no_key<Key>();
+                }
+            }
+        }
+        if constexpr (K == 8) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) list[i] = key[i];
+            if constexpr (C == 2) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) list[i] = max_key(list[i], key[15 - i]);
+                sort_bitonic(list);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) list[i] = key[i];
+            if constexpr (C == 2) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) list[8 + i] = key[15 - i];
+                sort_bitonic(list);
+            }
+        }
+        join_lanes<L, K>(list);
+
+        // the chosen ones: lane i (and i + L ..) of a token has the i-th
+        double weight[(K + L - 1) / L];
+        int expert[(K + L - 1) / L];
+        double d = 0.0;
+#pragma unroll
+        for (int u = 0; u < (K + L - 1) / L; ++u) {
+            Key own = no_key<Key>();
+#pragma unroll
+            for (int i = u * L; i < (u + 1) * L && i < K; ++i)
+                if (i == u * L + sub) own = list[i];
+            const bool there = !none && u * L + sub < a.top && own > no_key<Key>();
+            expert[u] = there ? key_expert(own) : -1;
+            float ze = 0.0f;
+            if (there) ze = widen<DT>(x[expert[u]]);
+            weight[u] = !there ? 0.0 : sigmoid ? sigmoid_of(ze) : share_to(ze, m);
+            if (!sigmoid && (EXACT || !a.renormalise)) weight[u] *= part;
+            d += weight[u];
+        }
+        d = lanes_sum<L>(d) + kTiny;
+        const bool some = !none && list[0] > no_key<Key>();
+        const double unit = static_cast<double>(a.scale) * (a.renormalise ? 1.0 / d : 1.0);
+        // a softmax of nothing but -inf; without a bias some expert is open else
+        const bool nan = live && (bad || (!sigmoid && (EXACT ? !(all > 0.0) : !some)));
+#pragma unroll
+        for (int u = 0; u < (K + L - 1) / L; ++u) {
+            const int i = u * L + sub;
+            if (i >= a.top || row >= a.x.rows) continue;
+            a.weights[row * a.top + i] = nan ? __builtin_nanf("") : static_cast<float>(weight[u] * unit);
+            a.ids[row * a.top + i] = expert[u];
+            if (sums && expert[u] >= 0) atomicAdd(&count[expert[u]], 1);
+        }
+        if (sums && some) {
+            const float f = EXACT && !sigmoid ? 1.0f : static_cast<float>(part);
+#pragma unroll
+            for (int i = 0; i < P; ++i) total[i] += static_cast<double>(s[i] * f);
+            if (sub == 0) {
+                ++tokens;
+                if (!sigmoid) {
+                    const double lse = static_cast<double>(m) + log_sum(all);
+                    squares += lse * lse;
+                }
             }
         }
     }
     if (!sums) return;
+    // a wave's tokens had the same lanes: their sums, then the waves', in this order
 #pragma unroll
-    for (int i = 0; i < P; ++i) c_of[wave][lane + i * kWave] = total[i];
+    for (int i = 0; i < P; ++i) {
+#pragma unroll
+        for (int o = L; o < kWave; o *= 2) total[i] += __shfl_xor(total[i], o);
+        if (slot == 0) reinterpret_cast<double*>(own_space)[(i / 8 * L + sub) * 8 + i % 8] = total[i];
+    }
+#pragma unroll
+    for (int o = 1; o < kWave; o *= 2) {
+        squares += __shfl_xor(squares, o);
+        tokens += __shfl_xor(tokens, o);
+    }
     if (lane == 0) {
         square[wave] = squares;
         routed[wave] = tokens;
@@ -266,51 +525,64 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a, RouteSums 
     double* share = w.share + int64_t(blockIdx.x) * (n + 1);
     int32_t* load = w.load + int64_t(blockIdx.x) * (n + 1);
     for (int e = threadIdx.x; e <= n; e += kRouteThreads) {
-        double s = 0.0;
+        double v = 0.0;
         int32_t c = e < n ? count[e] : 0;
 #pragma unroll
         for (int i = 0; i < kRouteWaves; ++i) {
-            s += e < n ? c_of[i][e] : square[i];
+            v += e < n ? reinterpret_cast<const double*>(space + i * space_bytes)[e] : square[i];
             if (e == n) c += routed[i];
         }
-        share[e] = s;
+        share[e] = v;
         load[e] = c;
     }
 }
 
-// The workgroups' sums joined in a fixed order, 8 experts a workgroup.
-constexpr int kFinishThreads = 256;
-constexpr int kFinishExperts = 8;
+// The workgroups' sums joined in a fixed order, 16 experts a workgroup: a row of a workgroup's sums is a
+// line of 128 bytes.
+constexpr int kFinishThreads = 1024;
+constexpr int kFinishExperts = 16;
 
 __global__ __launch_bounds__(kFinishThreads) void k_route_finish(RouteArgs a, RouteSums w)
 {
-    constexpr int SLICES = kFinishThreads / kFinishExperts;
+    constexpr int SLICES = kFinishThreads / kFinishExperts, U = 8;
     __shared__ double s_part[SLICES][kFinishExperts];
     __shared__ int64_t c_part[SLICES][kFinishExperts];
-    __shared__ int64_t n_part[SLICES][kFinishExperts];
+    __shared__ int64_t n_part[SLICES];
     const int n = a.x.vocab;
     const int col = threadIdx.x % kFinishExperts, slice = threadIdx.x / kFinishExperts;
-    const int e = static_cast<int>(blockIdx.x) * kFinishExperts + col;
+    const int e = min(static_cast<int>(blockIdx.x) * kFinishExperts + col, n);
     double s = 0.0;
     int64_t c = 0, t = 0;
-    for (int g = slice; g < w.groups; g += SLICES) {
-        if (e <= n) {
-            s += w.share[int64_t(g) * (n + 1) + e];
-            c += w.load[int64_t(g) * (n + 1) + e];
+    for (int from = slice; from < w.groups; from += U * SLICES) {
+        double v[U];
+        int32_t k[U], r[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int g = min(from + u * SLICES, w.groups - 1);
+            v[u] = w.share[int64_t(g) * (n + 1) + e];
+            k[u] = w.load[int64_t(g) * (n + 1) + e];
+            r[u] = w.load[int64_t(g) * (n + 1) + n];
         }
-        t += w.load[int64_t(g) * (n + 1) + n];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (from + u * SLICES >= w.groups) continue;
+            s += v[u];
+            c += k[u];
+            t += r[u];
+        }
     }
     s_part[slice][col] = s;
     c_part[slice][col] = c;
-    n_part[slice][col] = t;
+    if (col == 0) n_part[slice] = t;
     __syncthreads();
-    if (slice != 0 || e > n) return;
+    if (slice != 0 || static_cast<int>(blockIdx.x) * kFinishExperts + col > n) return;
     s = 0.0;
     c = t = 0;
+#pragma unroll 8
     for (int i = 0; i < SLICES; ++i) {
         s += s_part[i][col];
         c += c_part[i][col];
-        t += n_part[i][col];
+        t += n_part[i];
     }
     a.load[e] = c;
     const double mean = t > 0 ? s / static_cast<double>(t) : 0.0;
@@ -318,34 +590,42 @@ __global__ __launch_bounds__(kFinishThreads) void k_route_finish(RouteArgs a, Ro
     if (e == n && a.aux != nullptr) a.aux[1] = static_cast<float>(mean);
 }
 
-__global__ __launch_bounds__(kFinishThreads) void k_route_aux(RouteArgs a)
+__global__ __launch_bounds__(kRouteThreads) void k_route_aux(RouteArgs a)
 {
-    __shared__ double part[kFinishThreads / kWave];
+    __shared__ double part[kRouteWaves];
     const int n = a.x.vocab;
     double s = 0.0;
-    for (int e = threadIdx.x; e < n; e += kFinishThreads)
+    for (int e = threadIdx.x; e < n; e += kRouteThreads)
         s += static_cast<double>(a.load[e]) * static_cast<double>(a.share[e]);
     s = lanes_sum<kWave>(s);
     if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = s;
     __syncthreads();
     if (threadIdx.x != 0) return;
     s = 0.0;
-    for (int i = 0; i < kFinishThreads / kWave; ++i) s += part[i];
+    for (int i = 0; i < kRouteWaves; ++i) s += part[i];
     const double tokens = static_cast<double>(a.load[n]);
     a.aux[0] = tokens > 0.0 ? static_cast<float>(s * n / (a.top * tokens)) : 0.0f;
 }
 
-// One wave per token.  With F the factor over the tokens routed, pull_e = F balance E load_e / (k N)
-// and ds the gradient of the chosen experts' scores,
+// With F the factor over the tokens routed, pull_e = F balance E load_e / (k N) and ds the gradient of
+// the chosen experts' scores,
 //   softmax  dx_e = s_e (pull_e + ds_e - sum_j s_j (pull_j + ds_j) + 2 F z lse)
 //   sigmoid  dx_e = s_e (1 - s_e) ((pull_e - sum_j p_j pull_j) / sum s + ds_e),    p = s / sum s.
-template <int DT, int P, bool SIGMOID>
+// L lanes per token and P experts a lane, as in the choice.
+template <int DT, int L, int P, bool SIGMOID>
 __global__ __launch_bounds__(kRouteThreads) void k_route_grad(RouteGradArgs a)
 {
     using T = typename Fmt<DT>::T;
-    __shared__ float extra[kRouteWaves][P * kWave];
+    constexpr int E = Fmt<DT>::E;
+    constexpr int R = kWave / L, C = P / 8, N = L * P;
+    constexpr int U = (MP_ROUTE_MAX_TOP + L - 1) / L;          // chosen experts a lane
+    __shared__ float extra_of[kRouteWaves][R][N];              // ds by expert; 0 between tokens
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const int sub = lane % L, slot = lane / L;
     const int n = a.x.vocab;
+    float* const extra = extra_of[wave][slot];
+#pragma unroll
+    for (int i = 0; i < P; ++i) extra[i * L + sub] = 0.0f;
     double factor = 0.0;
     float pull[P] = {};
     if (a.load != nullptr) {
@@ -354,124 +634,178 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_grad(RouteGradArgs a)
         const double unit = factor * static_cast<double>(a.balance) * n / a.top /
                             static_cast<double>(tokens > 0 ? tokens : 1);
 #pragma unroll
-        for (int i = 0; i < P; ++i)
-            if (lane + i * kWave < n)
-                pull[i] = static_cast<float>(unit * static_cast<double>(a.load[lane + i * kWave]));
+        for (int i = 0; i < P; ++i) {
+            const int e = (i / 8 * L + sub) * 8 + i % 8;
+            if (e < n) pull[i] = static_cast<float>(unit * static_cast<double>(a.load[e]));
+        }
     }
     const double large = 2.0 * factor * static_cast<double>(a.large);
-    for (int64_t row = int64_t(blockIdx.x) * kRouteWaves + wave; row < a.x.rows;
-         row += int64_t(gridDim.x) * kRouteWaves) {
+    const int64_t step = int64_t(gridDim.x) * kRouteWaves * R;
+    for (int64_t first = (int64_t(blockIdx.x) * kRouteWaves + wave) * R; first < a.x.rows; first += step) {
+        const int64_t row = first + slot;
+        const bool in = row < a.x.rows;
+        const bool live = in && (a.mask == nullptr || a.mask[row] != 0);
         const T* x = static_cast<const T*>(a.x.x) + row * a.x.stride;
         T* dx = static_cast<T*>(a.g.dx) + row * a.g.stride;
+        int64_t id[U];
+        float dw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = u * L + sub;
+            id[u] = live && i < a.top ? a.ids[row * a.top + i] : -1;
+            dw[u] = a.dweights != nullptr && id[u] >= 0 ? a.dweights[row * a.top + i] * a.scale : 0.0f;
+        }
         float z[P];
-        const bool live = a.mask == nullptr || a.mask[row] != 0;
-        bool bad = false;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            if (live) load8<DT>(x, (c * L + sub) * 8, n, z + c * 8);
+            else
+                for (int j = 0; j < 8; ++j) z[c * 8 + j] = -__builtin_inff();
+        }
         float m = -FLT_MAX;
-        if (live) {
+        bool bad = false, any = false;
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const int e = lane + i * kWave;
-                z[i] = e < n ? widen<DT>(x[e]) : -__builtin_inff();
-                bad |= z[i] != z[i] || (!SIGMOID && z[i] == __builtin_inff());
-                m = __builtin_fmaxf(m, z[i]);
-            }
+        for (int u = 0; u < U; ++u) {
+            bad |= id[u] >= n;
+            if (id[u] >= n) id[u] = -1;
+            any |= id[u] >= 0;
         }
-        int64_t id = -1;
-        float dw = 0.0f;
-        if (live && lane < a.top) {
-            id = a.ids[row * a.top + lane];
-            if (a.dweights != nullptr && id >= 0)
-                dw = a.dweights[row * a.top + lane] * a.scale;
-        }
-        const bool past = id >= n;
-        if (past) id = -1;
-        m = lanes_max<kWave>(m);
-        float s[P], slope[P];            // slope: ds_e / dx_e of a sigmoid
-        double all = 0.0;
-        if (live) {
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                if (SIGMOID) {
-                    const float u = exp2_hw(-__builtin_fabsf(z[i]) * static_cast<float>(kLog2E));
-                    const float r = 1.0f / (1.0f + u);
-                    s[i] = z[i] >= 0.0f ? r : u * r;
-                    slope[i] = u * r * r;
-                } else {
-                    s[i] = exp2_hw((z[i] - m) * static_cast<float>(kLog2E));
-                }
-                all += static_cast<double>(s[i]);
-            }
+        for (int i = 0; i < P; ++i) {
+            bad |= z[i] != z[i];
+            m = __builtin_fmaxf(m, z[i]);
         }
-        all = lanes_sum<kWave>(all);
-        const bool nan = __builtin_amdgcn_ballot_w64(bad || past) != 0 || (live && !SIGMOID && !(all > 0.0));
-        const bool any = __builtin_amdgcn_ballot_w64(id >= 0) != 0;
-        if (!live || nan || !any) {
-            const float v = live && nan ? __builtin_nanf("") : 0.0f;
+        m = lanes_max<L>(m);
+        bad = lanes_max<L>(bad ? 1.0f : 0.0f) > 0.0f || (!SIGMOID && m == __builtin_inff());
+        any = lanes_max<L>(any ? 1.0f : 0.0f) > 0.0f;
+        float s[P], slope[SIGMOID ? P : 1];        // slope: ds_e / dx_e of a sigmoid
+        float lane_sum = 0.0f;
+        auto score = [](float v, float& u) {       // a sigmoid, and exp(-|v|) over 1 + that, squared
+            const float t = exp2_hw(-__builtin_fabsf(v) * static_cast<float>(kLog2E));
+            const float r = 1.0f / (1.0f + t);
+            u = t * r * r;
+            return v >= 0.0f ? r : t * r;
+        };
 #pragma unroll
-            for (int i = 0; i < P; ++i)
-                if (lane + i * kWave < n) store_one<DT>(dx + lane + i * kWave, v);
-            continue;
+        for (int i = 0; i < P; ++i) {
+            if constexpr (SIGMOID) s[i] = score(z[i], slope[i]);
+            else s[i] = share_to_fast(z[i], m);
+            lane_sum += s[i];
         }
+        const double all = lanes_sum<L>(static_cast<double>(lane_sum));
+        const bool nan = live && (bad || (!SIGMOID && !(all > 0.0)));
+        const bool on = live && any && !nan;
         const float part = all > 0.0 ? static_cast<float>(1.0 / all) : 0.0f;
         // the chosen experts' scores and their gradient
-        float ws = 0.0f;
-        if (id >= 0) {
-            const float ze = widen<DT>(x[id]);
-            if (SIGMOID) {
-                const float u = exp2_hw(-__builtin_fabsf(ze) * static_cast<float>(kLog2E));
-                ws = (ze >= 0.0f ? 1.0f : u) / (1.0f + u);
-            } else {
-                ws = exp2_hw((ze - m) * static_cast<float>(kLog2E)) * part;
-            }
-        }
-        double ds = static_cast<double>(dw);
+        double ds[U];
         if (a.renormalise) {
-            const double d = lanes_sum<kWave>(static_cast<double>(ws)) + kTiny;
-            const double mean = lanes_sum<kWave>(static_cast<double>(dw) * static_cast<double>(ws)) / d;
-            ds = id >= 0 ? (static_cast<double>(dw) - mean) / d : 0.0;
-        }
+            float ws[U];
+            double d = 0.0, mean = 0.0;
 #pragma unroll
-        for (int i = 0; i < P; ++i) extra[wave][lane + i * kWave] = 0.0f;
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        // the same expert twice: its parts add up, in the list's order
-        double same = 0.0;
-        for (int i = 0; i < a.top; ++i) {
-            const int64_t other = __shfl(id, i);
-            const double part_of = __shfl(ds, i);
-            if (other == id) same += part_of;
-        }
-        if (id >= 0) extra[wave][id] = static_cast<float>(same);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        double dot = 0.0;
-        float to[P];
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-            to[i] = extra[wave][lane + i * kWave];
-            if (!SIGMOID) {
-                s[i] *= part;
-                to[i] += pull[i];
-                dot += static_cast<double>(s[i]) * static_cast<double>(to[i]);
-            } else {
-                dot += static_cast<double>(s[i]) * static_cast<double>(pull[i]);
+            for (int u = 0; u < U; ++u) {
+                float unused;
+                const float ze = id[u] >= 0 ? widen<DT>(x[id[u]]) : -__builtin_inff();
+                if constexpr (SIGMOID) ws[u] = score(ze, unused);
+                else ws[u] = share_to_fast(ze, m) * part;
+                if (id[u] < 0) ws[u] = 0.0f;
+                d += static_cast<double>(ws[u]);
+                mean += static_cast<double>(dw[u]) * static_cast<double>(ws[u]);
             }
-        }
-        dot = lanes_sum<kWave>(dot);
-        float base;
-        if (SIGMOID) base = all > 0.0 ? static_cast<float>(dot / all) : 0.0f;
-        else base = static_cast<float>(large * (static_cast<double>(m) + log_sum(all)) - dot);
+            d = lanes_sum<L>(d) + kTiny;
+            mean = lanes_sum<L>(mean) / d;
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const int e = lane + i * kWave;
-            const float v = SIGMOID ? slope[i] * ((pull[i] - base) * part + to[i]) : s[i] * (to[i] + base);
-            if (e < n) store_one<DT>(dx + e, v);
+            for (int u = 0; u < U; ++u) ds[u] = id[u] >= 0 ? (static_cast<double>(dw[u]) - mean) / d : 0.0;
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) ds[u] = static_cast<double>(dw[u]);
+        }
+        // each writes its own number where its ds will be: an expert that is there twice shows
+        wave_fence();
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (id[u] >= 0) extra[id[u]] = __int_as_float(u * L + sub + 1);
+        wave_fence();
+        bool twice = false;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (id[u] >= 0) twice |= __float_as_int(extra[id[u]]) != u * L + sub + 1;
+        wave_fence();
+        if (__builtin_amdgcn_ballot_w64(twice) != 0) {
+            // its parts add up, in the list's order
+            double same[U] = {};
+            for (int i = 0; i < a.top; ++i) {
+#pragma unroll
+                for (int v = 0; v < U; ++v) {
+                    if (i / L != v) continue;
+                    const int from = slot * L + i % L;
+                    const int64_t other = __shfl(id[v], from);
+                    const double part_of = __shfl(ds[v], from);
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        if (other == id[u]) same[u] += part_of;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) ds[u] = same[u];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (id[u] >= 0) extra[id[u]] = static_cast<float>(ds[u]);
+        wave_fence();
+        float to[P];
+        double dot = 0.0;
+        {
+            float lane_dot = 0.0f;
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                to[i] = extra[(i / 8 * L + sub) * 8 + i % 8];
+                if constexpr (!SIGMOID) {
+                    s[i] *= part;
+                    to[i] += pull[i];
+                    lane_dot = __builtin_fmaf(s[i], to[i], lane_dot);
+                } else {
+                    lane_dot = __builtin_fmaf(s[i], pull[i], lane_dot);
+                }
+            }
+            dot = lanes_sum<L>(static_cast<double>(lane_dot));
+        }
+        wave_fence();
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (id[u] >= 0) extra[id[u]] = 0.0f;
+        float base;
+        if constexpr (SIGMOID) base = all > 0.0 ? static_cast<float>(dot / all) : 0.0f;
+        else base = static_cast<float>((large != 0.0 ? large * (static_cast<double>(m) + log_sum(all)) : 0.0) - dot);
+        const float off = nan ? __builtin_nanf("") : 0.0f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int e = (c * L + sub) * 8;
+            float f[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int i = c * 8 + j;
+                if constexpr (SIGMOID) f[j] = slope[i] * ((pull[i] - base) * part + to[i]);
+                else f[j] = s[i] * (to[i] + base);
+                if (!on) f[j] = off;
+            }
+            if (!in) continue;
+            if (e + 8 <= n) {
+#pragma unroll
+                for (int j = 0; j < 8; j += E)
+                    store_vec<DT>(dx + e + j, pack<DT>(reinterpret_cast<const float(&)[E]>(f[j])));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (e + j < n) store_one<DT>(dx + e + j, f[j]);
+            }
         }
     }
 }
 
 // out = bias + speed sign(mean load - load), one workgroup a layer; a skipped step leaves the bias.
-__global__ __launch_bounds__(kFinishThreads) void k_route_bias(RouteBiasArgs a)
+__global__ __launch_bounds__(kRouteThreads) void k_route_bias(RouteBiasArgs a)
 {
-    __shared__ int64_t part[kFinishThreads / kWave];
+    __shared__ int64_t part[kRouteWaves];
     const int64_t layer = blockIdx.x;
     const int n = a.experts;
     const bool skip = a.skipped != nullptr && *a.skipped != 0;
@@ -481,94 +815,117 @@ __global__ __launch_bounds__(kFinishThreads) void k_route_bias(RouteBiasArgs a)
         return c;
     };
     int64_t all = 0;
-    for (int e = threadIdx.x; e < n; e += kFinishThreads) all += load_of(e);
+    for (int e = threadIdx.x; e < n; e += kRouteThreads) all += load_of(e);
 #pragma unroll
     for (int d = 1; d < kWave; d *= 2) all += __shfl_xor(all, d);
     if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = all;
     __syncthreads();
     all = 0;
 #pragma unroll
-    for (int i = 0; i < kFinishThreads / kWave; ++i) all += part[i];
-    for (int e = threadIdx.x; e < n; e += kFinishThreads) {
+    for (int i = 0; i < kRouteWaves; ++i) all += part[i];
+    for (int e = threadIdx.x; e < n; e += kRouteThreads) {
         const int64_t off = all - load_of(e) * n;
         const float step = skip || off == 0 ? 0.0f : off > 0 ? a.speed : -a.speed;
         a.out[layer * n + e] = a.bias[layer * n + e] + step;
     }
 }
 
-template <int DT, int P>
-void route_p(const RouteArgs& a, const RouteSums& w, unsigned grid, hipStream_t s)
+// Workgroups of a launch over the tokens.
+int64_t route_grid(int64_t rows, int lanes, int64_t most)
 {
-    if (a.sigmoid) k_route<DT, P, true><<<grid, kRouteThreads, 0, s>>>(a, w);
-    else k_route<DT, P, false><<<grid, kRouteThreads, 0, s>>>(a, w);
+    const int per = kRouteWaves * (kWave / lanes);
+    const int64_t grid = (rows + per - 1) / per;
+    return grid < most ? grid : most;
+}
+
+template <int DT, int L, int P, int K, bool EXACT>
+void route_shape(const RouteArgs& a, RouteSums& w, hipStream_t s)
+{
+    int64_t most = 1 << 16;
+    if (a.load != nullptr) {
+        most = MP_ROUTE_WORKSPACE_BYTES / (12 * (int64_t(a.x.vocab) + 1));
+        if (most > 1024) most = 1024;
+    }
+    const int64_t grid = route_grid(a.x.rows, L, most);
+    if (a.load != nullptr) {
+        w.groups = static_cast<int>(grid);
+        w.share = static_cast<double*>(a.workspace);
+        w.load = reinterpret_cast<int32_t*>(w.share + grid * (a.x.vocab + 1));
+    }
+    if (grid == 0) return;
+    constexpr int R = kWave / L, N = L * P;
+    constexpr int key_bytes = EXACT || DT == kFP32 ? 8 : 4;
+    int space = 0;
+    if (a.groups > 1) space = R * ((group_keys(a.x.vocab, a.groups, N) + a.groups) * key_bytes + a.groups);
+    if (a.load != nullptr && space < N * 8) space = N * 8;
+    space = (space + 15) / 16 * 16;
+    k_route<DT, L, P, K, EXACT>
+        <<<static_cast<unsigned>(grid), kRouteThreads, static_cast<unsigned>(space * kRouteWaves), s>>>(a, w, space);
+}
+
+template <int DT, int K, bool EXACT>
+void route_key(const RouteArgs& a, RouteSums& w, hipStream_t s)
+{
+    if (a.x.vocab <= 64) route_shape<DT, 8, 8, K, EXACT>(a, w, s);
+    else if (a.x.vocab <= 128) route_shape<DT, 8, 16, K, EXACT>(a, w, s);
+    else if (a.x.vocab <= 256) route_shape<DT, 16, 16, K, EXACT>(a, w, s);
+    else if (a.x.vocab <= 512) route_shape<DT, 32, 16, K, EXACT>(a, w, s);
+    else route_shape<DT, 64, 16, K, EXACT>(a, w, s);
 }
 
 template <int DT>
-void route_dt(const RouteArgs& a, const RouteSums& w, unsigned grid, hipStream_t s)
+void route_dt(const RouteArgs& a, RouteSums& w, hipStream_t s)
 {
-    if (a.x.vocab <= 64) route_p<DT, 1>(a, w, grid, s);
-    else if (a.x.vocab <= 256) route_p<DT, 4>(a, w, grid, s);
-    else route_p<DT, 16>(a, w, grid, s);
+    const bool exact = a.bias != nullptr || (a.groups > 1 && a.group_best == 2);
+    if (a.top <= 8) exact ? route_key<DT, 8, true>(a, w, s) : route_key<DT, 8, false>(a, w, s);
+    else exact ? route_key<DT, 16, true>(a, w, s) : route_key<DT, 16, false>(a, w, s);
 }
 
-template <int DT, int P>
-void grad_p(const RouteGradArgs& a, unsigned grid, hipStream_t s)
+template <int DT, int L, int P>
+void grad_shape(const RouteGradArgs& a, hipStream_t s)
 {
-    if (a.sigmoid) k_route_grad<DT, P, true><<<grid, kRouteThreads, 0, s>>>(a);
-    else k_route_grad<DT, P, false><<<grid, kRouteThreads, 0, s>>>(a);
+    const unsigned grid = static_cast<unsigned>(route_grid(a.x.rows, L, 4096));
+    if (a.sigmoid) k_route_grad<DT, L, P, true><<<grid, kRouteThreads, 0, s>>>(a);
+    else k_route_grad<DT, L, P, false><<<grid, kRouteThreads, 0, s>>>(a);
 }
 
 template <int DT>
-void grad_dt(const RouteGradArgs& a, unsigned grid, hipStream_t s)
+void grad_dt(const RouteGradArgs& a, hipStream_t s)
 {
-    if (a.x.vocab <= 64) grad_p<DT, 1>(a, grid, s);
-    else if (a.x.vocab <= 256) grad_p<DT, 4>(a, grid, s);
-    else grad_p<DT, 16>(a, grid, s);
+    if (a.x.vocab <= 64) grad_shape<DT, 8, 8>(a, s);
+    else if (a.x.vocab <= 128) grad_shape<DT, 8, 16>(a, s);
+    else if (a.x.vocab <= 256) grad_shape<DT, 16, 16>(a, s);
+    else if (a.x.vocab <= 512) grad_shape<DT, 32, 16>(a, s);
+    else grad_shape<DT, 64, 16>(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_route(const RouteArgs& a, int dtype, hipStream_t s)
 {
-    const int64_t per = 12 * (int64_t(a.x.vocab) + 1);
-    int64_t most = a.load != nullptr ? MP_ROUTE_WORKSPACE_BYTES / per : 1 << 16;
-    if (a.load != nullptr && most > 1024) most = 1024;
-    int64_t grid = (int64_t(a.x.rows) + kRouteWaves - 1) / kRouteWaves;
-    if (grid > most) grid = most;
     RouteSums w{};
+    if (dtype == kBF16) route_dt<kBF16>(a, w, s);
+    else if (dtype == kFP16) route_dt<kFP16>(a, w, s);
+    else route_dt<kFP32>(a, w, s);
     if (a.load != nullptr) {
-        w.groups = static_cast<int>(grid);
-        w.share = static_cast<double*>(a.workspace);
-        w.load = reinterpret_cast<int32_t*>(w.share + grid * (a.x.vocab + 1));
-    }
-    if (grid > 0) {
-        const unsigned g = static_cast<unsigned>(grid);
-        if (dtype == kBF16) route_dt<kBF16>(a, w, g, s);
-        else if (dtype == kFP16) route_dt<kFP16>(a, w, g, s);
-        else route_dt<kFP32>(a, w, g, s);
-    }
-    if (a.load != nullptr) {
-        const unsigned cols = (static_cast<unsigned>(a.x.vocab) + kFinishExperts) / kFinishExperts;
+        const unsigned cols = static_cast<unsigned>(a.x.vocab) / kFinishExperts + 1;
         k_route_finish<<<cols, kFinishThreads, 0, s>>>(a, w);
-        if (a.aux != nullptr) k_route_aux<<<1, kFinishThreads, 0, s>>>(a);
+        if (a.aux != nullptr) k_route_aux<<<1, kRouteThreads, 0, s>>>(a);
     }
     return hipGetLastError();
 }
 
 hipError_t launch_route_grad(const RouteGradArgs& a, int dtype, hipStream_t s)
 {
-    int64_t grid = (int64_t(a.x.rows) + kRouteWaves - 1) / kRouteWaves;
-    if (grid > 4096) grid = 4096;
-    const unsigned g = static_cast<unsigned>(grid);
-    if (dtype == kBF16) grad_dt<kBF16>(a, g, s);
-    else if (dtype == kFP16) grad_dt<kFP16>(a, g, s);
-    else grad_dt<kFP32>(a, g, s);
+    if (dtype == kBF16) grad_dt<kBF16>(a, s);
+    else if (dtype == kFP16) grad_dt<kFP16>(a, s);
+    else grad_dt<kFP32>(a, s);
     return hipGetLastError();
 }
 
 hipError_t launch_route_bias(const RouteBiasArgs& a, hipStream_t s)
 {
-    k_route_bias<<<static_cast<unsigned>(a.layers), kFinishThreads, 0, s>>>(a);
+    k_route_bias<<<static_cast<unsigned>(a.layers), kRouteThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 

@@ -1,9 +1,14 @@
 """Routing to experts from its definitions, in binary64 with numpy, and how far a result of the
 library may be off (``tol_*``), from the arithmetic it documents.
 
-Choices are by binary64 numbers rounded to 42 bits: what is equal but for the order of a sum is equal.  Weights, shares and losses are formed in binary64 and rounded once to fp32,
-but for a logarithm good to 2^-23.  The gradient is formed in fp32 from shares with a relative error of
-E = 4 u (|z| + 2), z the logit (softmax: its difference to the largest), u = 2^-24.
+Choices are by binary64 numbers rounded to 42 bits: what is equal but for the order of a sum is equal.
+Without a bias and without sums of two scores the order is the logits', also where scores round alike.
+A chosen expert's own exponential is binary64's.  What is summed over the experts (a softmax's sum,
+the shares) may be fp32 with a relative error of E = 4 u (|z| + 2), z the logit (softmax: its difference
+to the largest), u = 2^-24: an exponent of two roundings of its size, an exponential good to one step; so
+is the gradient, formed in fp32.  A sum over a token's experts is then off by the mean of E over the
+shares, a share by that, its own E and four roundings; a weight that is not divided by the chosen
+ones' sum by the softmax's sum.
 """
 import numpy as np
 
@@ -33,7 +38,7 @@ def scores(x, sigmoid):
 
 def route(x, bias, mask, sigmoid, top, groups=1, top_groups=1, best=1, renormalise=True, scale=1.0):
     rows, n = x.shape
-    s, lse, _ = scores(x, sigmoid)
+    s, lse, E = scores(x, sigmoid)
     bad = np.isnan(x).any(1)
     if not sigmoid:
         bad |= np.isposinf(x).any(1) | np.isneginf(x).all(1)
@@ -41,7 +46,8 @@ def route(x, bias, mask, sigmoid, top, groups=1, top_groups=1, best=1, renormali
     with np.errstate(all="ignore"):
         c = s + (0.0 if bias is None else bias)
     open_ = (x > -np.inf) & (c > -np.inf)
-    cr = rounded(c)
+    by_logit = bias is None and (groups == 1 or best == 1)
+    cr = x if by_logit else rounded(c)
     ids = np.full((rows, top), -1)
     w = np.zeros((rows, top))
     for r in range(rows):
@@ -53,9 +59,9 @@ def route(x, bias, mask, sigmoid, top, groups=1, top_groups=1, best=1, renormali
         may = open_[r].copy()
         if groups > 1:
             width = n // groups
-            val = []                    # of the unrounded
+            val = []
             for g in range(groups):
-                cs = sorted(c[r, g * width:(g + 1) * width][may[g * width:(g + 1) * width]], reverse=True)
+                cs = sorted(cr[r, g * width:(g + 1) * width][may[g * width:(g + 1) * width]], reverse=True)
                 val.append(float(rounded(sum(cs[:best]))) if cs else -np.inf)
             order = sorted(range(groups), key=lambda g: (-val[g], g))[top_groups:]
             for g in order:
@@ -75,10 +81,15 @@ def route(x, bias, mask, sigmoid, top, groups=1, top_groups=1, best=1, renormali
     share = p.sum(0) / tokens if len(p) else np.zeros(n)
     aux = np.array([n * (load[:n] * share).sum() / (top * tokens),
                     (lse[ok] ** 2).sum() / tokens if not sigmoid else 0.0])
+    with np.errstate(all="ignore"):
+        sum_off = np.nan_to_num((s * E).sum(1) / s.sum(1)) + 2 * U
+    off_w = np.abs(w) * (1e-13 if sigmoid or renormalise else sum_off[:, None])
+    off_p = (p * (E[ok] + sum_off[ok][:, None] + 4 * U)).sum(0) / tokens if len(p) else 0.0 * share
+    off_lse = (2 * np.abs(lse[ok]) * (sum_off[ok] + 2 * U)).sum() / tokens if not sigmoid else 0.0
     return dict(ids=ids, weights=w, load=load, share=share, aux=aux,
-                tol_weights=round_tol(w) + np.abs(w) * 1e-13,
-                tol_share=round_tol(share) + share * 1e-12,
-                tol_aux=round_tol(aux) + np.array([aux[0] * 2 * U, 4 * U * np.sqrt(aux[1]) + 1e-12 * aux[1]]))
+                tol_weights=round_tol(w) + off_w, tol_share=round_tol(share) + off_p,
+                tol_aux=round_tol(aux) + np.array([
+                    n * (load[:n] * (off_p + share * U)).sum() / (top * tokens) + aux[0] * 2 * U, off_lse]))
 
 
 def loss(x, ids, mask, dweights, load, sigmoid, top, renormalise, scale, balance, large, factor):
