@@ -1,17 +1,21 @@
 // HIP kernels of the scores of logits: log-probability, entropy and the likeliest
 // entries of a row, and the gradient of the first two.
 //
-// With k = log2(e) / T as the nearest float kf plus a rest and a lane's reference
-// R = fl(m kf), m its maximum, one fma gives y_j = x_j kf - R, and a lane sums
-//   s = sum_j 2^y_j,   c = sum_j y_j 2^y_j,
-// both rescaled when m grows.  R's rounding and kf's are the same for all of a row's
-// elements, so they drop out of the shares q_j but for a factor near 1 of known
-// logarithm: with d = R - m kf,
+// With k = log2(e) / T as the nearest float kf plus a rest, and a lane's reference R near its
+// largest logit's exponent, one fma gives y_j = x_j kf - R, and a lane sums
+//   s = sum_j 2^y_j,   c = sum_j y_j 2^y_j.
+// Both are scaled down, and R raised, only where a logit exceeds R by kSlack: the sums need not
+// be relative to the maximum, but near it.  What R and kf are off is the same for all of a row's
+// elements, so it drops out of the shares q_j but for a factor near 1 of known logarithm:
+// with m the row's maximum and d = R - m kf,
 //   log2 S = log2 s + d + (rest / kf) (c / s + d)     (S = sum_j 2^((x_j - m) k)),
 //   lse = m / T + ln S,   lp = (x_t - m) / T - ln S,   H = ln S - (c / s + d) / (kf T).
-// That saves two operations a logit against differences x_j - m; a row whose largest
+// That takes fewer operations a logit than differences x_j - m do; a row whose largest
 // logit reaches 2^24 / kf, where R's steps are no longer small, is summed again from
 // differences.
+//
+// The passes are bound by HBM and the vector units alike: 6.5 TB/s of 16-bit logits leave 12 lane
+// operations a logit, and its exponential counts for four of them.
 #include <float.h>
 
 #include "rows.h"
@@ -20,8 +24,11 @@
 namespace mpk {
 namespace {
 
+constexpr float kSlack = 8.0f;           // of an exponent over its reference
+
 struct RowScale {
     float k;               // the float nearest to log2(e) / T
+    float slack;           // kSlack of an exponent as a difference of logits
     double rest;           // log2(e) / T - k
     double inv_t;
 };
@@ -31,6 +38,7 @@ __device__ __forceinline__ RowScale scale_of(const LogitsView& x)
     const double whole = static_cast<double>(x.k_hi) + static_cast<double>(x.k_lo);
     RowScale r;
     r.k = static_cast<float>(whole);
+    r.slack = static_cast<float>(static_cast<double>(kSlack) / whole);
     r.rest = whole - static_cast<double>(r.k);
     r.inv_t = x.inv_t;
     return r;
@@ -43,18 +51,16 @@ constexpr float kGone = -200.0f;         // an exponent whose power of two is 0
 // A lane's sums.  m starts at the lowest finite value: -inf never enters a difference.
 struct Share {
     float m = -FLT_MAX;
+    float most = -FLT_MAX;               // the logit that raises the reference
     float ref = 0.0f;
     float s = 0.0f, c = 0.0f;
 };
 
-// N elements; returns their maximum.
-template <int N>
-__device__ __forceinline__ float add(Share& a, const float (&f)[N], float k)
+// The reference raised where a maximum g asks for it.
+__device__ __forceinline__ void raise(Share& a, float g, float k, float slack)
 {
-    float g = f[0];
-#pragma unroll
-    for (int i = 1; i < N; ++i) g = __builtin_fmaxf(g, f[i]);
-    if (g > a.m) {
+    a.m = __builtin_fmaxf(a.m, g);
+    if (g > a.most) {
         // an unlikely row's references may be limited; none is infinite, so nothing here is NaN
         const float r = __builtin_amdgcn_fmed3f(g * k, -kRefMost, kRefMost);
         const float d = __builtin_amdgcn_fmed3f(a.ref - r, kGone, 0.0f);
@@ -62,14 +68,90 @@ __device__ __forceinline__ float add(Share& a, const float (&f)[N], float k)
         a.c = __builtin_fmaf(a.s, d, a.c) * down;
         a.s *= down;
         a.ref = r;
-        a.m = g;
+        a.most = g + slack;
     }
+}
+
+template <int N>
+__device__ __forceinline__ void add_shares(Share& a, const float (&f)[N], float k)
+{
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const float y = __builtin_fmaf(f[i], k, -a.ref);
         const float e = exp2_hw(y);                    // NaN stays NaN
         a.s += e;
-        a.c = __builtin_fmaf(e, __builtin_fmaxf(y, kGone), a.c);      // 0, not 0 * -inf
+        a.c = __builtin_fmaf(e, y, a.c);
+    }
+}
+
+// c again where it met 0 * -inf, of a mask or of an overflow downwards: these add 0.
+template <int N>
+__device__ __forceinline__ float add_masked(const Share& a, float c, const float (&f)[N], float k)
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float y = __builtin_fmaf(f[i], k, -a.ref);
+        c = __builtin_fmaf(exp2_hw(y), __builtin_fmaxf(y, kGone), c);
+    }
+    return c;
+}
+
+__device__ __forceinline__ void add_one(Share& a, float f, float k, float slack)
+{
+    const float one[1] = {f};
+    raise(a, f, k, slack);
+    const float before = a.c;
+    add_shares(a, one, k);
+    if (a.c != a.c) a.c = add_masked(a, before, one, k);
+}
+
+// The largest of two vectors' elements.  fp16 ones are compared two at a time: the sums then take
+// them as they are (v_fma_mix_f32), and none is widened.
+template <int DT>
+__device__ __forceinline__ float max_of(u32x4 a, u32x4 b)
+{
+    if constexpr (DT == kFP16) {
+        f16x2 h[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t u = a[i], v = b[i];
+            h[i] = __builtin_bit_cast(f16x2, u);
+            h[4 + i] = __builtin_bit_cast(f16x2, v);
+        }
+#pragma unroll
+        for (int i = 1; i < 8; ++i) h[0] = __builtin_elementwise_max(h[0], h[i]);
+        return __builtin_fmaxf(static_cast<float>(h[0].x), static_cast<float>(h[0].y));
+    } else {
+        constexpr int E = Fmt<DT>::E;
+        float f[E], g[E];
+        unpack<DT>(a, f);
+        unpack<DT>(b, g);
+        float m = __builtin_fmaxf(f[0], g[0]);
+#pragma unroll
+        for (int i = 1; i < E; ++i) m = __builtin_fmaxf(__builtin_fmaxf(m, f[i]), g[i]);
+        return m;
+    }
+}
+
+// Two vectors; returns their maximum.
+template <int DT>
+__device__ __forceinline__ float add_pair(Share& s, u32x4 a, u32x4 b, const RowScale& k)
+{
+    constexpr int E = Fmt<DT>::E;
+    const float g = max_of<DT>(a, b);
+    raise(s, g, k.k, k.slack);
+    const float before = s.c;
+    float f[E];
+    unpack<DT>(a, f);
+    add_shares(s, f, k.k);
+    unpack<DT>(b, f);
+    add_shares(s, f, k.k);
+    if (s.c != s.c) {
+        asm volatile("" : "+v"(a), "+v"(b));           // unpacked again, not kept for this
+        unpack<DT>(a, f);
+        s.c = add_masked(s, before, f, k.k);
+        unpack<DT>(b, f);
+        s.c = add_masked(s, s.c, f, k.k);
     }
     return g;
 }
@@ -87,7 +169,7 @@ __device__ __forceinline__ void add_to(Share& a, const float (&f)[N], float k)
     }
 }
 
-// A row's statistics, in all lanes.
+// A row's statistics.
 struct RowStat {
     float m;
     double ln_s;          // of the sum relative to m
@@ -113,7 +195,7 @@ struct JoinSpace {
     double s[THREADS / kWave], c[THREADS / kWave];
 };
 
-// All lanes' shares, valid in all lanes.
+// All lanes' shares joined: m valid in all lanes, the sums in the first wave's.
 template <int THREADS>
 __device__ __forceinline__ void join(const Share& a, JoinSpace<THREADS>& l, float& m, float& ref, double& s,
                                      double& c)
@@ -136,10 +218,14 @@ __device__ __forceinline__ void join(const Share& a, JoinSpace<THREADS>& l, floa
         }
         __syncthreads();
         m = l.m[lane % W];
-        ref = l.ref[lane % W];
-        s = l.s[lane % W];
-        c = l.c[lane % W];
-        join_lanes<W>(m, ref, s, c);
+        if (wave == 0) {
+            ref = l.ref[lane % W];
+            s = l.s[lane % W];
+            c = l.c[lane % W];
+            join_lanes<W>(m, ref, s, c);
+        } else {
+            m = lanes_max<W>(m);
+        }
     }
 }
 
@@ -165,22 +251,29 @@ __device__ __forceinline__ uint32_t order_of(float v)
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Entries in their order -- the larger logit first, of equal ones the lower id -- as whole numbers, the
-// first the largest.  0 comes after every entry.
+// Entries in their order -- the larger logit first, of equal ones the lower id (below 2^30) -- as whole
+// numbers of 62 bits, the first the largest.  0 comes after every entry.
+constexpr int kIdBits = 30;
+constexpr uint32_t kIdMost = (1u << kIdBits) - 1;
+
 __device__ __forceinline__ uint64_t entry_key(float v, int id)
 {
-    return uint64_t(order_of(v)) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(id));
+    return uint64_t(order_of(v)) << kIdBits | (kIdMost - static_cast<uint32_t>(id));
+}
+
+__device__ __forceinline__ float order_value(uint32_t up)
+{
+    return __uint_as_float(up & 0x80000000u ? up & 0x7FFFFFFFu : ~up);
 }
 
 __device__ __forceinline__ float key_value(uint64_t key)
 {
-    const uint32_t up = static_cast<uint32_t>(key >> 32);
-    return __uint_as_float(up & 0x80000000u ? up & 0x7FFFFFFFu : ~up);
+    return order_value(static_cast<uint32_t>(key >> kIdBits));
 }
 
 __device__ __forceinline__ int key_id(uint64_t key)
 {
-    return static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(key));
+    return static_cast<int>(kIdMost - (static_cast<uint32_t>(key) & kIdMost));
 }
 
 // What a workgroup goes over: the vectors [lo, hi) of a row, and the elements that lanes take singly.
@@ -216,18 +309,22 @@ struct Piece {
 // maxima is a bound that at least k elements reach, and few more: k elements fall into different
 // lanes mostly.  So the slots that reach it name the few vectors that are read again, and what of them
 // reaches it is ranked by counting, as (logit, id) in one whole number.
-constexpr int kSlots = 32;
-
 template <int THREADS>
 struct Lists {
-    static constexpr int kKeys = 8 * THREADS, kHits = 4 * THREADS;
+    static constexpr int kKeys = THREADS < 256 ? 8 * THREADS : 2048, kHits = kKeys / 2;
+    static constexpr int kSlots = 4 * kKeys / THREADS;           // of a lane
     union {
         uint16_t slot[kSlots * THREADS];
         uint64_t key[kKeys];
     };
-    uint32_t hit[kHits];
+    union {
+        uint16_t hit[kHits];
+        uint32_t count[256];
+    };
     uint32_t lane_max[THREADS];
-    int hits, keys, above, bin;
+    uint16_t lane[THREADS];              // the lanes that reach the bound
+    uint32_t bound;
+    int lanes, hits, keys, above, bin;
 };
 
 template <int THREADS>
@@ -239,21 +336,14 @@ __device__ __forceinline__ void put_key(Lists<THREADS>& l, uint64_t key)
 
 // Shares of a piece's vectors, and with TOP the slots; `per` pairs to a slot.
 template <int DT, int THREADS, bool TOP, bool NT>
-__device__ __forceinline__ void piece_sums(Share& share, const Piece<DT>& p, float k, Lists<THREADS>& l, int per)
+__device__ __forceinline__ void piece_sums(Share& share, const Piece<DT>& p, const RowScale& k,
+                                           Lists<THREADS>& l, int per)
 {
-    constexpr int E = Fmt<DT>::E, U = 4;
+    constexpr int U = 4;
     const int tid = threadIdx.x;
     int slot = tid, left = per;
-    auto pair = [&](u32x4 a, u32x4 b, bool in_a, bool in_b) {
-        float f[2][E];
-        unpack<DT>(a, f[0]);
-        unpack<DT>(b, f[1]);
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-            if (!in_a) f[0][j] = -__builtin_inff();
-            if (!in_b) f[1][j] = -__builtin_inff();
-        }
-        const float g = add(share, reinterpret_cast<const float(&)[2 * E]>(f), k);
+    auto pair = [&](u32x4 a, u32x4 b) {
+        const float g = add_pair<DT>(share, a, b, k);
         if constexpr (TOP) {
             uint16_t o = static_cast<uint16_t>(order_of(g) >> 16);
             if (left != per) o = max(o, l.slot[slot]);
@@ -270,18 +360,24 @@ __device__ __forceinline__ void piece_sums(Share& share, const Piece<DT>& p, flo
 #pragma unroll
         for (int u = 0; u < U; ++u) v[u] = load_vec<DT, NT>(p.at(base + u * THREADS + tid));
 #pragma unroll
-        for (int u = 0; u < U; u += 2) pair(v[u], v[u + 1], true, true);
+        for (int u = 0; u < U; u += 2) pair(v[u], v[u + 1]);
     }
     for (; base < p.hi; base += 2 * THREADS) {
+        constexpr uint32_t gone = DT == kBF16 ? 0xFF80FF80u : DT == kFP16 ? 0xFC00FC00u : 0xFF800000u;     // -inf
         const int i = base + tid, j = i + THREADS;
-        const u32x4 a = load_vec<DT, NT>(p.at(min(i, p.hi - 1)));
-        const u32x4 b = load_vec<DT, NT>(p.at(min(j, p.hi - 1)));
-        pair(a, b, i < p.hi, j < p.hi);
+        u32x4 a = load_vec<DT, NT>(p.at(min(i, p.hi - 1)));
+        u32x4 b = load_vec<DT, NT>(p.at(min(j, p.hi - 1)));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (i >= p.hi) a[e] = gone;
+            if (j >= p.hi) b[e] = gone;
+        }
+        pair(a, b);
     }
 }
 
 // A bound on the order that at least k of the workgroup's lane maxima reach and not many more: found
-// bit by bit, by every wave alike.
+// bit by bit, by one wave.
 template <int THREADS>
 __device__ __forceinline__ uint32_t lane_bound(const Lists<THREADS>& l, int k)
 {
@@ -309,7 +405,7 @@ __device__ __forceinline__ uint32_t lane_bound(const Lists<THREADS>& l, int k)
         for (int i = 0; i < N; ++i) c += __builtin_popcountll(__builtin_amdgcn_ballot_w64(v[i] >= trial));
         if (c < k) continue;
         bound = trial;
-        if (c <= k + k / 4 + 2) break;
+        if (c <= k + k / 16 + 1) break;
     }
     return max(bound, 0x00800000u);                           // -inf is no entry
 }
@@ -320,7 +416,7 @@ __device__ __forceinline__ uint32_t lane_bound(const Lists<THREADS>& l, int k)
 template <int DT, int THREADS>
 __device__ __forceinline__ void choose_by_passes(const Piece<DT>& p, int k, Lists<THREADS>& l)
 {
-    uint32_t* const count = l.hit;
+    uint32_t* const count = l.count;
     uint64_t prefix = 0, bound;
     int before = 0;
     for (int shift = 56;; shift -= 8) {
@@ -376,8 +472,11 @@ __device__ __forceinline__ void emit_ranked(const Lists<THREADS>& l, int n, int 
 {
     for (int i = threadIdx.x; i < n; i += THREADS) {
         const uint64_t own = l.key[i];
+        // 62 bits are a positive finite binary64 number, whose comparison is the faster one
+        const double o = __builtin_bit_cast(double, own);
         int rank = 0;
-        for (int j = 0; j < n; ++j) rank += l.key[j] > own;
+#pragma unroll 8
+        for (int j = 0; j < n; ++j) rank += __builtin_bit_cast(double, l.key[j]) > o;
         if (rank < k) emit(rank, own);
     }
     for (int i = n + static_cast<int>(threadIdx.x); i < k; i += THREADS) emit(i, uint64_t(0));
@@ -389,76 +488,86 @@ __device__ __forceinline__ void choose(const Piece<DT>& p, float lane_max, int p
 {
     constexpr int E = Fmt<DT>::E;
     const int tid = threadIdx.x;
-    l.lane_max[tid] = order_of(lane_max);
-    if (tid == 0) l.hits = l.keys = 0;
+    const uint32_t own = order_of(lane_max);
+    l.lane_max[tid] = own;
+    if (tid == 0) l.lanes = l.hits = l.keys = 0;
     __syncthreads();
-    const uint32_t bound = lane_bound(l, k);
+    if (tid < kWave) {
+        const uint32_t b = lane_bound(l, k);
+        if (tid == 0) l.bound = b;
+    }
+    __syncthreads();
+    const uint32_t bound = l.bound;
+    const float least = order_value(bound);
+    if (own >= bound) l.lane[atomicAdd(&l.lanes, 1)] = static_cast<uint16_t>(tid);
+    __syncthreads();
     const int pairs = (p.hi - p.lo + 2 * THREADS - 1) / (2 * THREADS);
     const int slots = (pairs + per - 1) / per;
-    for (int i = 0; i < slots; ++i)
-        if (l.slot[i * THREADS + tid] >= bound >> 16) {
-            const int at = atomicAdd(&l.hits, 1);
-            if (at < Lists<THREADS>::kHits) l.hit[at] = i * THREADS + tid;
+    const int lanes = l.lanes;
+    for (int i = tid / 16; i < lanes; i += THREADS / 16)
+        for (int q = tid % 16; q < slots; q += 16) {
+            const int at = q * THREADS + l.lane[i];
+            if (l.slot[at] >= bound >> 16) {
+                const int h = atomicAdd(&l.hits, 1);
+                if (h < Lists<THREADS>::kHits) l.hit[h] = static_cast<uint16_t>(at);
+            }
         }
     __syncthreads();                          // from here on keys take the slots' place
     const int hits = l.hits;
     if (hits <= Lists<THREADS>::kHits) {
         const int each = 2 * per;
         for (int i = tid; i < hits * each; i += THREADS) {
-            const int h = static_cast<int>(l.hit[i / each]);
+            const int h = l.hit[i / each];
             const int vec = p.lo + (h / THREADS * each + i % each) * THREADS + h % THREADS;
             if (vec >= p.hi) continue;
             float v[E];
             unpack<DT>(load_vec<DT, false>(p.at(vec)), v);
 #pragma unroll
             for (int j = 0; j < E; ++j)
-                if (order_of(v[j]) >= bound) put_key(l, entry_key(v[j], p.head + vec * E + j));
+                if (v[j] >= least) put_key(l, entry_key(v[j], p.head + vec * E + j));
         }
-        if (p.one >= 0 && order_of(p.single) >= bound) put_key(l, entry_key(p.single, p.one));
+        if (p.one >= 0 && p.single >= least) put_key(l, entry_key(p.single, p.one));
         __syncthreads();
     }
     if (hits > Lists<THREADS>::kHits || l.keys > Lists<THREADS>::kKeys) choose_by_passes(p, k, l);
     emit_ranked(l, l.keys, k, emit);
 }
 
-// The sums of a piece, in all lanes: relative to 2^ref.
+// The sums of a piece, relative to 2^ref (in the first wave; m in all lanes).
 struct PieceStat {
     double ref, s, c;
     float m;
 };
 
 template <int DT, int THREADS, bool TOP>
-__device__ __forceinline__ PieceStat piece_stat(const Piece<DT>& p, float k, bool stream, int per,
+__device__ __forceinline__ PieceStat piece_stat(const Piece<DT>& p, const RowScale& k, bool stream, int per,
                                                 Lists<THREADS>& l, JoinSpace<THREADS>& space, float& lane_max)
 {
     Share share;
     if (stream) piece_sums<DT, THREADS, TOP, true>(share, p, k, l, per);
     else piece_sums<DT, THREADS, TOP, false>(share, p, k, l, per);
-    if (p.one >= 0) {
-        const float f[1] = {p.single};
-        add(share, f, k);
-    }
+    if (p.one >= 0) add_one(share, p.single, k.k, k.slack);
     lane_max = share.m;
     PieceStat r;
     float ref;
     join<THREADS>(share, space, r.m, ref, r.s, r.c);
     r.ref = static_cast<double>(ref);
-    if (!(__builtin_fabsf(r.m * k) < kRowMost)) {
+    if (!(__builtin_fabsf(r.m * k.k) < kRowMost)) {
         share = Share{};
         share.m = r.m;
         p.template each<THREADS>([&](float v, int) {
             const float f[1] = {v};
-            add_to(share, f, k);
+            add_to(share, f, k.k);
         });
         join<THREADS>(share, space, r.m, ref, r.s, r.c);
-        r.ref = static_cast<double>(r.m) * static_cast<double>(k);
+        r.ref = static_cast<double>(r.m) * static_cast<double>(k.k);
     }
     return r;
 }
 
 __device__ __forceinline__ void write_entry(const ScoreArgs& a, int64_t at, uint64_t key, const RowStat& r)
 {
-    const bool there = key != 0;
+    const bool there = key != 0 && r.ln_s == r.ln_s;
     const float v = there ? key_value(key) : -__builtin_inff();
     a.top_ids[at] = there ? key_id(key) : -1;
     if (a.top_values != nullptr) a.top_values[at] = v;
@@ -492,7 +601,7 @@ __device__ __forceinline__ void write_off(const ScoreArgs& a, int64_t row)
 
 // One row per workgroup.
 template <int DT, int THREADS, bool TOP>
-__global__ __launch_bounds__(THREADS) void k_scores(ScoreArgs a, int per)
+__global__ __launch_bounds__(THREADS, 8) void k_scores(ScoreArgs a, int per)
 {
     using T = typename Fmt<DT>::T;
     __shared__ JoinSpace<THREADS> space;
@@ -514,17 +623,19 @@ __global__ __launch_bounds__(THREADS) void k_scores(ScoreArgs a, int per)
     const float xt = target < n ? widen<DT>(x[target]) : 0.0f;
     float lane_max;
     auto& l = reinterpret_cast<Lists<THREADS>&>(lists);
-    const PieceStat st = piece_stat<DT, THREADS, TOP>(p, k.k, a.x.stream, per, l, space, lane_max);
-    const RowStat r = stat_of(st.m, st.ref, st.s, st.c, k);
-    if (threadIdx.x == 0) write_row(a, row, target, xt, r);
-    if constexpr (TOP) {
-        auto emit = [&](int rank, uint64_t key) { write_entry(a, row * a.top + rank, key, r); };
-        if (r.ln_s == r.ln_s) {
-            choose<DT, THREADS>(p, lane_max, per, a.top, l, emit);
-        } else {
-            for (int e = threadIdx.x; e < a.top; e += THREADS) emit(e, 0);
+    const PieceStat st = piece_stat<DT, THREADS, TOP>(p, k, a.x.stream, per, l, space, lane_max);
+    __shared__ RowStat whole;
+    if (threadIdx.x < kWave) {
+        const RowStat r = stat_of(st.m, st.ref, st.s, st.c, k);
+        if (threadIdx.x == 0) {
+            write_row(a, row, target, xt, r);
+            whole = r;                       // the choice has barriers before anything is emitted
         }
     }
+    if constexpr (TOP)
+        choose<DT, THREADS>(p, lane_max, per, a.top, l, [&](int rank, uint64_t key) {
+            write_entry(a, row * a.top + rank, key, whole);
+        });
 }
 
 // Few rows, less than the chip has room for: a row is cut into parts, one workgroup each, that leave
@@ -560,7 +671,7 @@ __global__ __launch_bounds__(kPartThreads) void k_score_parts(ScoreArgs a, Score
     p.single = p.one >= 0 ? widen<DT>(x[p.one]) : 0.0f;
     float lane_max;
     auto& l = reinterpret_cast<Lists<kPartThreads>&>(lists);
-    const PieceStat st = piece_stat<DT, kPartThreads, TOP>(p, k.k, false, per, l, space, lane_max);
+    const PieceStat st = piece_stat<DT, kPartThreads, TOP>(p, k, false, per, l, space, lane_max);
     if (threadIdx.x == 0) w.stat[blockIdx.x] = st;
     if constexpr (TOP)
         choose<DT, kPartThreads>(p, lane_max, per, a.top, l, [&](int rank, uint64_t key) {
@@ -580,8 +691,20 @@ __global__ __launch_bounds__(kPartThreads) void k_score_join(ScoreArgs a, ScoreP
     if (target < 0) return write_off(a, row);
     const RowScale k = scale_of(a.x);
     const float xt = target < n ? widen<DT>(x[target]) : 0.0f;
+    // all loads before anything waits for one: the parts' sums, the lists and their deep entries
     PieceStat st{-__builtin_inf(), 0.0, 0.0, -FLT_MAX};
     if (lane < w.parts) st = w.stat[row * w.parts + lane];
+    constexpr int kEach = Lists<kPartThreads>::kKeys / kPartThreads;
+    const int entries = w.parts * a.top;                   // at most kKeys
+    uint64_t key[TOP ? kEach : 1], bound = ~uint64_t(0);
+    if constexpr (TOP) {
+        const uint64_t* list = w.key + row * entries;
+        // of P sorted lists the k / P-th entries: at least k entries reach the smallest of them
+        const int deep = (a.top + w.parts - 1) / w.parts - 1;
+        if (lane < w.parts) bound = list[lane * a.top + deep];
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) key[i] = i * kPartThreads + tid < entries ? list[i * kPartThreads + tid] : 0;
+    }
     const float m = lanes_max<kWave>(st.m);
     // a part without any element in reach has no say in the reference; a NaN's is kept
     double ref = st.s != 0.0 ? st.ref : -__builtin_inf();
@@ -599,14 +722,6 @@ __global__ __launch_bounds__(kPartThreads) void k_score_join(ScoreArgs a, ScoreP
     if (tid == 0) write_row(a, row, target, xt, r);
     if constexpr (TOP) {
         auto& l = reinterpret_cast<Lists<kPartThreads>&>(lists);
-        const uint64_t* key = w.key + row * w.parts * a.top;
-        if (r.ln_s != r.ln_s) {
-            for (int e = tid; e < a.top; e += kPartThreads) write_entry(a, row * a.top + e, 0, r);
-            return;
-        }
-        // of P sorted lists the k / P-th entries: at least k entries reach the smallest of them
-        const int deep = (a.top + w.parts - 1) / w.parts - 1;
-        uint64_t bound = lane < w.parts ? key[lane * a.top + deep] : ~uint64_t(0);
 #pragma unroll
         for (int e = 1; e < kWave; e *= 2) {
             const uint64_t o = __shfl_xor(bound, e);
@@ -615,10 +730,9 @@ __global__ __launch_bounds__(kPartThreads) void k_score_join(ScoreArgs a, ScoreP
         if (bound == 0) bound = 1;                     // an empty place is no entry
         if (tid == 0) l.keys = 0;
         __syncthreads();
-        for (int i = tid; i < w.parts * a.top; i += kPartThreads) {
-            const uint64_t v = key[i];
-            if (v >= bound) put_key(l, v);             // at most parts * top <= kKeys
-        }
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+            if (key[i] >= bound) put_key(l, key[i]);
         __syncthreads();
         emit_ranked(l, l.keys, a.top,
                     [&](int rank, uint64_t v) { write_entry(a, row * a.top + rank, v, r); });
@@ -705,10 +819,12 @@ __global__ __launch_bounds__(kGradThreads) void k_score_grad(ScoreGradArgs a, in
 }
 
 // Pairs that share a slot where `vecs` vectors are dealt to `threads` lanes.
-int pairs_per_slot(int vecs, int threads)
+template <int THREADS>
+int pairs_per_slot(int vecs)
 {
-    const int pairs = (vecs + 2 * threads - 1) / (2 * threads);
-    const int per = (pairs + kSlots - 1) / kSlots;
+    constexpr int slots = Lists<THREADS>::kSlots;
+    const int pairs = (vecs + 2 * THREADS - 1) / (2 * THREADS);
+    const int per = (pairs + slots - 1) / slots;
     return per > 0 ? per : 1;
 }
 
@@ -716,7 +832,7 @@ template <int DT, int THREADS>
 void whole_rows(const ScoreArgs& a, hipStream_t s)
 {
     const unsigned rows = static_cast<unsigned>(a.x.rows);
-    const int per = pairs_per_slot(a.x.vocab / Fmt<DT>::E, THREADS);
+    const int per = pairs_per_slot<THREADS>(a.x.vocab / Fmt<DT>::E);
     if (a.top > 0) k_scores<DT, THREADS, true><<<rows, THREADS, 0, s>>>(a, per);
     else k_scores<DT, THREADS, false><<<rows, THREADS, 0, s>>>(a, per);
 }
@@ -753,7 +869,7 @@ void scores_dt(ScoreArgs a, hipStream_t s)
     ScoreParts w;
     if (split<DT>(a, &w)) {
         const unsigned rows = static_cast<unsigned>(a.x.rows), all = rows * static_cast<unsigned>(w.parts);
-        const int per = pairs_per_slot(w.vecs, kPartThreads);
+        const int per = pairs_per_slot<kPartThreads>(w.vecs);
         if (a.top > 0) {
             k_score_parts<DT, true><<<all, kPartThreads, 0, s>>>(a, w, per);
             k_score_join<DT, true><<<rows, kPartThreads, 0, s>>>(a, w);

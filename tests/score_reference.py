@@ -9,9 +9,12 @@ A lane adds at most `chain` shares, one at a time, and scales its sums when the 
 exponential and a product, for which 2 chain stands); shares of lanes are joined in binary64 with one
 exponential each.  The sum is off by ds = sum_j q_j E_j + (3 chain + 16) u, its logarithm by ds + 2 u.
 
+R is up to 8 below the maximum's exponent: |y| is at most |z_j - max| log2(e) + 8 there, which adds
+8 ln 2 u = 5.6 u to E_j's exponent part (4 u (.. + 2) has 8 u).
+
 The entropy is ln S - sum_j q_j (z_j - max): the second term is off by E_j, ds and the roundings of
-its own chain of additions, (chain + 4) u, of sum_j q_j |z_j - max|, and k's rest tilts the shares: u
-times the variance of z in all.
+its own chain of additions, (chain + 4) u, of sum_j q_j (|z_j - max| + 5.6), and k's rest tilts the
+shares: u times the variance of z in all.
 """
 import numpy as np
 
@@ -29,7 +32,7 @@ def score(x, targets, T=1.0, top=0):
         mean = (q * a).sum(1)
         entropy = ln_s + mean
         var = (q * (a - mean[:, None]) ** 2).sum(1)
-        dh = ds + 2 * U + (q * a * E).sum(1) + mean * (ds + (chain + 4) * U) + 2 * U * var
+        dh = ds + 2 * U + (q * (a + 5.6) * E).sum(1) + (mean + 5.6) * (ds + (chain + 4) * U) + 2 * U * var
     live = np.ones(rows, bool) if targets is None else targets >= 0
     none = ~np.isfinite(ln_s)           # no distribution
     out = dict(lse=np.where(live, lse, 0.0), entropy=np.where(live, entropy, 0.0))
