@@ -25,48 +25,71 @@ namespace {
 
 constexpr double kLog2E = 1.4426950408889634;
 
-// 2^y for -1100 <= y <= 1000: the fraction's power by Chebyshev interpolation of degree 10 on [-1/2, 1/2]
-// (relative error 3e-16), the whole part as the exponent.  The library's exp takes twice the operations.
+// a b + c with c in scalar registers: the compiler would rather move c into vector registers first.
+__device__ __forceinline__ double fma_const(double a, double b, double c)
+{
+    double r;
+    asm("v_fma_f64 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "s"(c));
+    return r;
+}
+
+// 2^t for |t| <= 1/2 by Chebyshev interpolation of degree 10 (relative error 3e-16).  The library's exp
+// takes twice the operations.
+__device__ __forceinline__ double exp2_fraction(double t)
+{
+    double p = t * 7.072585949269224e-09 + 1.0208690299958306e-07;
+    p = fma_const(p, t, 1.321544258792169e-06);
+    p = fma_const(p, t, 1.5252657260200837e-05);
+    p = fma_const(p, t, 0.0001540353044173605);
+    p = fma_const(p, t, 0.0013333558230164974);
+    p = fma_const(p, t, 0.009618129107606888);
+    p = fma_const(p, t, 0.05550410866444772);
+    p = fma_const(p, t, 0.24022650695910097);
+    p = fma_const(p, t, 0.69314718055995);
+    return fma_const(p, t, 1.0);
+}
+
+// 2^y for -1100 <= y <= 1000.
 __device__ __forceinline__ double exp2_series(double y)
 {
     const double whole = __builtin_rint(y);
-    const double t = y - whole;
-    double p = 7.072585949269224e-09;
-    p = __builtin_fma(p, t, 1.0208690299958306e-07);
-    p = __builtin_fma(p, t, 1.321544258792169e-06);
-    p = __builtin_fma(p, t, 1.5252657260200837e-05);
-    p = __builtin_fma(p, t, 0.0001540353044173605);
-    p = __builtin_fma(p, t, 0.0013333558230164974);
-    p = __builtin_fma(p, t, 0.009618129107606888);
-    p = __builtin_fma(p, t, 0.05550410866444772);
-    p = __builtin_fma(p, t, 0.24022650695910097);
-    p = __builtin_fma(p, t, 0.69314718055995);
-    p = __builtin_fma(p, t, 1.0);
-    return __builtin_ldexp(p, static_cast<int>(whole));
+    return __builtin_ldexp(exp2_fraction(y - whole), static_cast<int>(whole));
 }
 
-// 1 / d for 1 <= d <= 2^1000 or so: the instruction's 2^-26 and two of Newton's steps.
+// exp(a) for |a| < 700: adding 1.5 2^52 leaves the exponent's whole part in the last bits.
+__device__ __forceinline__ double exp_tame(double a)
+{
+    constexpr double kWhole = 6755399441055744.0;
+    const double u = __builtin_fma(a, kLog2E, kWhole);
+    const double whole = u - kWhole;
+    const uint64_t p = __builtin_bit_cast(uint64_t, exp2_fraction(__builtin_fma(a, kLog2E, -whole)));
+    const uint32_t hi = static_cast<uint32_t>(p >> 32) + (static_cast<uint32_t>(__builtin_bit_cast(uint64_t, u)) << 20);
+    return __builtin_bit_cast(double, uint64_t(hi) << 32 | static_cast<uint32_t>(p));
+}
+
+// 1 / d for d in binary64's middle range: the instruction's 2^-24 and one of Newton's steps, or two.
+__device__ __forceinline__ double reciprocal_fast(double d)
+{
+    const double r = __builtin_amdgcn_rcp(d);
+    return __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+}
 __device__ __forceinline__ double reciprocal(double d)
 {
-    double r = __builtin_amdgcn_rcp(d);
-    r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+    const double r = reciprocal_fast(d);
     return __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
 }
 
-__device__ __forceinline__ double sigmoid_of(float z)
+// sigmoid(z), or exp(z - m) for z <= m, of any z.
+__device__ __forceinline__ double score_of(float z, float m, bool sigmoid)
 {
-    const double y = static_cast<double>(z) * -kLog2E;
-    return y > 1000.0 ? 0.0 : reciprocal(1.0 + exp2_series(y < -1000.0 ? -1000.0 : y));
+    const double a = sigmoid ? -static_cast<double>(z) : static_cast<double>(z) - static_cast<double>(m);
+    const double y = a * kLog2E;
+    const double e = exp2_series(y < -1100.0 ? -1100.0 : y > 1000.0 ? 1000.0 : y);
+    if (!sigmoid) return e;
+    return y > 1000.0 ? 0.0 : reciprocal(1.0 + e);
 }
 
-// exp(z - m), z <= m.
-__device__ __forceinline__ double share_to(float z, float m)
-{
-    const double y = (static_cast<double>(z) - static_cast<double>(m)) * kLog2E;
-    return exp2_series(y < -1100.0 ? -1100.0 : y);
-}
-
-// The same in fp32, relative error 2^-24 (|z - m| + 2): x log2(e) with the constant in two parts.
+// exp(z - m) in fp32, relative error 2^-24 (|z - m| + 2): x log2(e) with the constant in two parts.
 __device__ __forceinline__ float share_to_fast(float z, float m)
 {
     constexpr float hi = 1.44269502162933349609375f, lo = 1.925963033500e-8f;
@@ -76,12 +99,18 @@ __device__ __forceinline__ float share_to_fast(float z, float m)
 
 constexpr int kIdBits = 10;                              // MP_ROUTE_MAX_EXPERTS is 2^10
 constexpr uint64_t kIdMask = (1 << kIdBits) - 1;
-constexpr double kMost = 1e300;                          // so that no key is an infinity's or a NaN's
 
-// c (finite) as far as it counts: what is equal but for the rounding of sums is equal then.
+// A bias of an expert that is closed, and what a c is above that is open.  (Other biases are held below
+// 1e38 in size.)
+constexpr float kClosed = -FLT_MAX;
+constexpr float kBiasMost = 1e38f;
+constexpr double kOpen = -2e38;
+constexpr double kMost = 1e300;                          // the key of +inf: no key is a NaN's
+
+// c (finite, not -0) as far as it counts: what is equal but for the rounding of sums is equal then.
 __device__ __forceinline__ uint64_t rounded(double c)
 {
-    return (__builtin_bit_cast(uint64_t, c + 0.0) + (kIdMask + 1) / 2) & ~kIdMask;       // -0 is 0
+    return (__builtin_bit_cast(uint64_t, c) + (kIdMask + 1) / 2) & ~kIdMask;
 }
 
 // Keys of type double or uint32_t.
@@ -95,8 +124,19 @@ __device__ __forceinline__ Key no_key()
 // Of a negative c the larger last bits are the smaller number.
 __device__ __forceinline__ double key_of(double c, int e)
 {
-    const uint64_t u = rounded(c);
-    return __builtin_bit_cast(double, u | (u >> 63 ? uint64_t(e) : kIdMask - uint64_t(e)));
+    const uint64_t u = __builtin_bit_cast(uint64_t, c) + (kIdMask + 1) / 2;
+    const uint32_t hi = static_cast<uint32_t>(u >> 32);
+    const uint32_t sign = static_cast<uint32_t>(static_cast<int32_t>(hi) >> 31);
+    constexpr uint32_t mask = static_cast<uint32_t>(kIdMask);
+    const uint32_t last = (static_cast<uint32_t>(e) ^ mask) ^ (sign & mask);
+    return __builtin_bit_cast(double, uint64_t(hi) << 32 | ((static_cast<uint32_t>(u) & ~mask) | last));
+}
+
+template <class Key, bool EXACT>
+__device__ __forceinline__ bool is_open(Key key)
+{
+    if constexpr (EXACT) return key > kOpen;
+    else return key > no_key<Key>();
 }
 
 // A 16-bit logit's order in the upper half (never 0: -inf has no key).
@@ -219,12 +259,26 @@ constexpr double kTiny = 1e-20;
 struct RouteSums {
     double* share;
     int32_t* load;
+    double* part;       // for each workgroup that joins them: its part of the balance loss
+    int32_t* done;      // and how many of those are done: cleared by the first workgroup
     int groups;         // workgroups
 };
 
-// Eight neighbouring logits from element e of a row of n; -inf past its end.
+// Logits up to this size, and tokens whose largest is not below a quarter of it on that side, have
+// exponentials and sums in binary64's middle range.
+constexpr float kTame = 340.0f;
+
+// n, for comparisons that are formed where they are used and not, sixteen lane masks of them, kept over
+// a loop.
+__device__ __forceinline__ int here(int n)
+{
+    asm volatile("" : "+s"(n));
+    return n;
+}
+
+// Eight neighbouring logits from element e of a row of n; `past` past its end.
 template <int DT>
-__device__ __forceinline__ void load8(const typename Fmt<DT>::T* x, int e, int n, float* z)
+__device__ __forceinline__ void load8(const typename Fmt<DT>::T* x, int e, int n, float past, float* z)
 {
     constexpr int E = Fmt<DT>::E;
     if (e + 8 <= n) {
@@ -236,8 +290,9 @@ __device__ __forceinline__ void load8(const typename Fmt<DT>::T* x, int e, int n
             for (int j = 0; j < E; ++j) z[i + j] = f[j];
         }
     } else {
+        const int end = here(n);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) z[j] = e + j < n ? widen<DT>(x[e + j]) : -__builtin_inff();
+        for (int j = 0; j < 8; ++j) z[j] = e + j < end ? widen<DT>(x[e + j]) : past;
     }
 }
 
@@ -246,6 +301,13 @@ __device__ __forceinline__ void load8(const typename Fmt<DT>::T* x, int e, int n
 __device__ __forceinline__ void wave_fence()
 {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
+// Waves a SIMD that k_route's registers leave room for.
+template <int DT, int P, bool EXACT>
+constexpr int route_waves()
+{
+    return EXACT && P == 16 ? 2 : EXACT || DT == kFP32 ? 3 : 4;
 }
 
 // Places for keys that the groups of a token are formed from: two for each chunk, or all experts where
@@ -257,13 +319,15 @@ __host__ __device__ __forceinline__ int group_keys(int n, int groups, int all)
 
 // L lanes per token, P experts a lane: expert (c L + lane) 8 + j is the lane's P's c 8 + j.
 template <int DT, int L, int P, int K, bool EXACT>
-__global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a, RouteSums w, int space_bytes)
+__global__ __launch_bounds__(kRouteThreads, (route_waves<DT, P, EXACT>())) void k_route(RouteArgs a, RouteSums w, int space_bytes)
 {
     using T = typename Fmt<DT>::T;
     using Key = std::conditional_t<EXACT || DT == kFP32, double, uint32_t>;
     constexpr int R = kWave / L, C = P / 8, N = L * P;         // tokens a wave, chunks a lane, experts
     extern __shared__ __align__(16) char space[];       // a part for each wave
     __shared__ int32_t count[N];
+    __shared__ __align__(16) float bias_of[EXACT ? N : 1];
+    __shared__ uint8_t group_no[N];
     __shared__ double square[kRouteWaves];
     __shared__ int32_t routed[kRouteWaves];
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
@@ -278,71 +342,174 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a, RouteSums 
     Key* const group_of = mine + keys;
     uint8_t* const open_of = reinterpret_cast<uint8_t*>(reinterpret_cast<Key*>(own_space) + R * (keys + a.groups)) +
                              slot * a.groups;
-    double total[P] = {};
+    // A lane's sums are of at most some hundred tokens, fp32 (binary64 ones would take sixteen registers
+    // more than there are for three waves a SIMD); the lanes' are joined in binary64.
+    float total[P] = {};
     double squares = 0.0;
     int tokens = 0;
-    float bias[P] = {};
+    bool some_open = true;              // some expert that the bias leaves open
     if (sums) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) *w.done = 0;
         for (int e = threadIdx.x; e < N; e += kRouteThreads) count[e] = 0;
         __syncthreads();
     }
-    if constexpr (EXACT) {
-        if (a.bias != nullptr) {
-#pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const int e = (i / 8 * L + sub) * 8 + i % 8;
-                if (e < n) bias[i] = a.bias[e];
-            }
-        }
+    if (a.groups > 1) {
+        for (int e = threadIdx.x; e < N; e += kRouteThreads) group_no[e] = static_cast<uint8_t>(e < n ? e / width : 0);
+        __syncthreads();
     }
-    const int64_t step = int64_t(gridDim.x) * kRouteWaves * R;
-    for (int64_t first = (int64_t(blockIdx.x) * kRouteWaves + wave) * R; first < a.x.rows; first += step) {
-        const int64_t row = first + slot;
+    if constexpr (EXACT) {
+        some_open = false;
+        for (int e = threadIdx.x; e < N; e += kRouteThreads) {
+            const float v = e >= n ? -__builtin_inff() : a.bias != nullptr ? a.bias[e] : 0.0f;
+            bias_of[e] = v > -__builtin_inff() ? __builtin_amdgcn_fmed3f(v, -kBiasMost, kBiasMost) : kClosed;
+        }
+        __syncthreads();
+        for (int e = lane; e < N; e += kWave) some_open |= bias_of[e] > kClosed;
+        some_open = __builtin_amdgcn_ballot_w64(some_open) != 0;
+    }
+    const int step = static_cast<int>(gridDim.x) * kRouteWaves * R;        // rows are below 2^22
+    for (int first = (static_cast<int>(blockIdx.x) * kRouteWaves + wave) * R; first < a.x.rows; first += step) {
+        int row = first + slot;
+        asm volatile("" : "+v"(row));       // addresses are formed from it, not each kept and stepped
         const bool live = row < a.x.rows && (a.mask == nullptr || a.mask[row] != 0);
-        const T* x = static_cast<const T*>(a.x.x) + row * a.x.stride;
+        const T* x = static_cast<const T*>(a.x.x) + int64_t(row) * a.x.stride;
         float z[P];
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            if (live) load8<DT>(x, (c * L + sub) * 8, n, z + c * 8);
+            if (live) load8<DT>(x, (c * L + sub) * 8, n, EXACT ? -kTame : -__builtin_inff(), z + c * 8);
             else
-                for (int j = 0; j < 8; ++j) z[c * 8 + j] = -__builtin_inff();
+                for (int j = 0; j < 8; ++j) z[c * 8 + j] = 0.0f;
         }
         bool bad = false;
-        float m = -FLT_MAX;
+        float m = z[0];
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            bad |= z[i] != z[i];
-            m = __builtin_fmaxf(m, z[i]);
+        for (int i = 1; i < P; ++i) m = __builtin_fmaxf(m, z[i]);
+        m = __builtin_fmaxf(lanes_max<L>(m), -FLT_MAX);
+        // Are all logits of the wave's tokens of a size that needs no care?  (What is past a token's
+        // experts is at the lower end then, closed, and adds nothing that shows to a sum.)
+        bool tame = false;
+        if constexpr (EXACT) {
+            float lo = z[0], hi = z[0];
+#pragma unroll
+            for (int i = 1; i < P; ++i) {
+                lo = __builtin_fminf(lo, z[i]);
+                hi = __builtin_fmaxf(hi, z[i]);
+            }
+            bool odd = !(lo >= -kTame && hi <= kTame && m >= -kTame / 4);
+#pragma unroll
+            for (int i = 0; i < P; i += 2) odd |= __builtin_isunordered(z[i], z[i + 1]);
+            tame = __builtin_amdgcn_ballot_w64(odd) == 0;
         }
-        m = lanes_max<L>(m);
-        // +inf is the largest then; nothing but -inf leaves the sum 0
-        bad = lanes_max<L>(bad ? 1.0f : 0.0f) > 0.0f || (!sigmoid && m == __builtin_inff());
+        if (!tame) {
+            if constexpr (EXACT) {
+                m = -FLT_MAX;
+                const int end = here(n);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    if ((i / 8 * L + sub) * 8 + i % 8 >= end) z[i] = -__builtin_inff();
+                    m = __builtin_fmaxf(m, z[i]);
+                }
+                m = lanes_max<L>(m);
+            }
+#pragma unroll
+            for (int i = 0; i < P; i += 2) bad |= __builtin_isunordered(z[i], z[i + 1]);
+            // +inf is the largest then; nothing but -inf leaves the sum 0
+            bad = lanes_max<L>(bad ? 1.0f : 0.0f) > 0.0f || (!sigmoid && m == __builtin_inff());
+        }
 
         // the scores, where the choice or a sum over the tokens wants all of them
         Key key[P];
         double all = 0.0;
-        float s[P];                     // shares of a softmax, scores of a sigmoid: for the sums
+        bool some = live && some_open;  // is there an open expert?
         double part = 0.0;
         if constexpr (EXACT) {
-            double c[P];
+            float s[P];                  // shares of a softmax, scores of a sigmoid: for the sums
+            // four experts' arithmetic at a time: all sixteen at once would take all registers
+            auto four = [](int i) {
+                if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+            };
+            auto number = [&](int i) { return (i / 8 * L + sub) * 8 + i % 8; };
+            // and what the three ways below have in common is not formed before them
+            auto apart = [&](int i) { asm volatile("" : "+v"(z[i])::"memory"); };
+            if (tame && sigmoid) {
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                c[i] = sigmoid ? sigmoid_of(z[i]) : share_to(z[i], m);          // -inf: 0
-                all += c[i];
+                for (int i = 0; i < P; ++i) {
+                    apart(i);
+                    const double c = reciprocal_fast(1.0 + exp_tame(-static_cast<double>(z[i])));
+                    all += c;
+                    s[i] = static_cast<float>(c);
+                    key[i] = key_of(c + static_cast<double>(bias_of[number(i)]), number(i));
+                    four(i);
+                }
+                all = lanes_sum<L>(all);
+                part = reciprocal(all);
+            } else if (tame) {
+                const double top = static_cast<double>(m);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    apart(i);
+                    key[i] = exp_tame(static_cast<double>(z[i]) - top);
+                    all += key[i];
+                    four(i);
+                }
+                all = lanes_sum<L>(all);
+                part = reciprocal(all);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    const double c = key[i] * part;
+                    s[i] = static_cast<float>(c);
+                    key[i] = key_of(c + static_cast<double>(bias_of[number(i)]), number(i));
+                    four(i);
+                }
+            } else {
+                bool any = false;
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    apart(i);
+                    key[i] = score_of(z[i], m, sigmoid);
+                    all += key[i];
+                    four(i);
+                }
+                all = lanes_sum<L>(all);
+                part = all > 0.0 ? reciprocal(all) : 0.0;
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    const double c = sigmoid ? key[i] : key[i] * part;
+                    s[i] = bad ? 0.0f : static_cast<float>(c);         // NaN times 0 would be in the sums
+                    const float bias = z[i] > -__builtin_inff() ? bias_of[number(i)] : kClosed;
+                    any |= bias > kClosed;
+                    key[i] = key_of((bias > kClosed ? c : 0.0) + static_cast<double>(bias), number(i));
+                    four(i);
+                }
+                if (bad) part = 0.0;
+                some = live && !bad && lanes_max<L>(any ? 1.0f : 0.0f) > 0.0f;
             }
-            all = lanes_sum<L>(all);
-            part = all > 0.0 ? 1.0 / all : 0.0;
+            if (sums) {
+                const float f = !some ? 0.0f : sigmoid ? static_cast<float>(part) : 1.0f;
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                if (!sigmoid) c[i] *= part;
-                s[i] = static_cast<float>(c[i]);
-                double v = c[i] + static_cast<double>(bias[i]);
-                const bool in = z[i] > -__builtin_inff() && v > -__builtin_inf();
-                v = v < kMost ? v : kMost;
-                key[i] = in ? key_of(v, (i / 8 * L + sub) * 8 + i % 8) : no_key<Key>();
+                for (int i = 0; i < P; ++i) total[i] = __builtin_fmaf(s[i], f, total[i]);
             }
         } else {
+            bool any = false;
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const int e = (i / 8 * L + sub) * 8 + i % 8;
+                if constexpr (DT == kFP32) key[i] = key_of(static_cast<double>(z[i] + 0.0f), e);      // -0 is 0
+                else key[i] = key_of_logit<DT>(z[i], e);
+                const bool in = z[i] > -__builtin_inff();
+                any |= in;
+                if (!in) key[i] = no_key<Key>();
+            }
+            if constexpr (DT == kFP32) {
+                if (sigmoid && m == __builtin_inff()) {         // its key would be a NaN's
+#pragma unroll
+                    for (int i = 0; i < P; ++i)
+                        if (z[i] == __builtin_inff()) key[i] = key_of(kMost, (i / 8 * L + sub) * 8 + i % 8);
+                }
+            }
+            some = live && !bad && lanes_max<L>(any ? 1.0f : 0.0f) > 0.0f;
             if (sums || !(sigmoid || a.renormalise)) {
+                float s[P], lane_sum = 0.0f;         // shares of a softmax, scores of a sigmoid
 #pragma unroll
                 for (int i = 0; i < P; ++i) {
                     if (sigmoid) {
@@ -351,23 +518,14 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a, RouteSums 
                     } else {
                         s[i] = share_to_fast(z[i], m);
                     }
-                    all += static_cast<double>(s[i]);
+                    lane_sum += s[i];
                 }
-                all = lanes_sum<L>(all);
-                part = all > 0.0 ? 1.0 / all : 0.0;
-            }
+                all = lanes_sum<L>(static_cast<double>(lane_sum));
+                part = all > 0.0 ? reciprocal(all) : 0.0;
+                if (sums) {
+                    const float f = some ? static_cast<float>(part) : 0.0f;
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const int e = (i / 8 * L + sub) * 8 + i % 8;
-                if constexpr (DT == kFP32) key[i] = key_of(static_cast<double>(z[i]), e);
-                else key[i] = key_of_logit<DT>(z[i], e);
-                if (!(z[i] > -__builtin_inff())) key[i] = no_key<Key>();
-            }
-            if constexpr (DT == kFP32) {
-                if (sigmoid && m == __builtin_inff()) {         // its key would be a NaN's
-#pragma unroll
-                    for (int i = 0; i < P; ++i)
-                        if (z[i] == __builtin_inff()) key[i] = key_of(kMost, (i / 8 * L + sub) * 8 + i % 8);
+                    for (int i = 0; i < P; ++i) total[i] = __builtin_fmaf(some ? s[i] : 0.0f, f, total[i]);
                 }
             }
         }
@@ -397,9 +555,9 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a, RouteSums 
                     if (stride > 1) next = max_key(next, mine[(g * per + i) * stride + 1]);
                 }
                 if constexpr (EXACT) {
-                    if (a.group_best == 2 && best > no_key<Key>())
+                    if (a.group_best == 2 && is_open<Key, true>(best))
                         best = __builtin_bit_cast(
-                            double, rounded(key_score(best) + (next > no_key<Key>() ? key_score(next) : 0.0)));
+                            double, rounded(key_score(best) + (is_open<Key, true>(next) ? key_score(next) : 0.0)));
                 }
                 group_of[g] = best;
             }
@@ -420,7 +578,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a, RouteSums 
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 const int e = (i / 8 * L + sub) * 8 + i % 8;
-                if (e < n && !open_of[e / width]) key[i] = no_key<Key>();
+                if (!open_of[group_no[e]]) key[i] = no_key<Key>();
             }
         }
 #pragma unroll
@@ -435,7 +593,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a, RouteSums 
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 const int e = (c * L + sub) * 8;
-                if (e < n && !open_of[e / width]) {
+                if (!open_of[group_no[e]]) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) key[c * 8 + j] = no_key<Key>();
                 }
@@ -470,37 +628,31 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a, RouteSums 
 #pragma unroll
             for (int i = u * L; i < (u + 1) * L && i < K; ++i)
                 if (i == u * L + sub) own = list[i];
-            const bool there = !none && u * L + sub < a.top && own > no_key<Key>();
+            const bool there = !none && u * L + sub < a.top && is_open<Key, EXACT>(own);
             expert[u] = there ? key_expert(own) : -1;
             float ze = 0.0f;
             if (there) ze = widen<DT>(x[expert[u]]);
-            weight[u] = !there ? 0.0 : sigmoid ? sigmoid_of(ze) : share_to(ze, m);
+            weight[u] = there ? score_of(ze, m, sigmoid) : 0.0;
             if (!sigmoid && (EXACT || !a.renormalise)) weight[u] *= part;
             d += weight[u];
         }
         d = lanes_sum<L>(d) + kTiny;
-        const bool some = !none && list[0] > no_key<Key>();
-        const double unit = static_cast<double>(a.scale) * (a.renormalise ? 1.0 / d : 1.0);
+        const double unit = static_cast<double>(a.scale) * (a.renormalise ? reciprocal(d) : 1.0);
         // a softmax of nothing but -inf; without a bias some expert is open else
         const bool nan = live && (bad || (!sigmoid && (EXACT ? !(all > 0.0) : !some)));
 #pragma unroll
         for (int u = 0; u < (K + L - 1) / L; ++u) {
             const int i = u * L + sub;
             if (i >= a.top || row >= a.x.rows) continue;
-            a.weights[row * a.top + i] = nan ? __builtin_nanf("") : static_cast<float>(weight[u] * unit);
-            a.ids[row * a.top + i] = expert[u];
+            a.weights[int64_t(row) * a.top + i] = nan ? __builtin_nanf("") : static_cast<float>(weight[u] * unit);
+            a.ids[int64_t(row) * a.top + i] = expert[u];
             if (sums && expert[u] >= 0) atomicAdd(&count[expert[u]], 1);
         }
-        if (sums && some) {
-            const float f = EXACT && !sigmoid ? 1.0f : static_cast<float>(part);
-#pragma unroll
-            for (int i = 0; i < P; ++i) total[i] += static_cast<double>(s[i] * f);
-            if (sub == 0) {
-                ++tokens;
-                if (!sigmoid) {
-                    const double lse = static_cast<double>(m) + log_sum(all);
-                    squares += lse * lse;
-                }
+        if (sums && some && sub == 0) {
+            ++tokens;
+            if (!sigmoid) {
+                const double lse = static_cast<double>(m) + log_sum(all);
+                squares += lse * lse;
             }
         }
     }
@@ -508,9 +660,10 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a, RouteSums 
     // a wave's tokens had the same lanes: their sums, then the waves', in this order
 #pragma unroll
     for (int i = 0; i < P; ++i) {
+        double v = static_cast<double>(total[i]);
 #pragma unroll
-        for (int o = L; o < kWave; o *= 2) total[i] += __shfl_xor(total[i], o);
-        if (slot == 0) reinterpret_cast<double*>(own_space)[(i / 8 * L + sub) * 8 + i % 8] = total[i];
+        for (int o = L; o < kWave; o *= 2) v += __shfl_xor(v, o);
+        if (slot == 0) reinterpret_cast<double*>(own_space)[(i / 8 * L + sub) * 8 + i % 8] = v;
     }
 #pragma unroll
     for (int o = 1; o < kWave; o *= 2) {
@@ -537,19 +690,21 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a, RouteSums 
     }
 }
 
-// The workgroups' sums joined in a fixed order, 16 experts a workgroup: a row of a workgroup's sums is a
-// line of 128 bytes.
+// The workgroups' sums joined in a fixed order, 16 experts a workgroup (a row of a workgroup's sums is a
+// line of 128 bytes).  The last workgroup to be done joins what the balance loss takes of each: a launch
+// more would take 4 us.  (A release by few workgroups is cheap; by all those of a large grid it is not.)
 constexpr int kFinishThreads = 1024;
 constexpr int kFinishExperts = 16;
+constexpr int kFinishMost = MP_ROUTE_MAX_EXPERTS / kFinishExperts + 1;
 
 __global__ __launch_bounds__(kFinishThreads) void k_route_finish(RouteArgs a, RouteSums w)
 {
-    constexpr int SLICES = kFinishThreads / kFinishExperts, U = 8;
-    __shared__ double s_part[SLICES][kFinishExperts];
-    __shared__ int64_t c_part[SLICES][kFinishExperts];
-    __shared__ int64_t n_part[SLICES];
-    const int n = a.x.vocab;
+    constexpr int SLICES = kFinishThreads / kFinishExperts, W = kFinishThreads / kWave, U = 4;
+    __shared__ double s_part[W][kFinishExperts];
+    __shared__ int64_t c_part[W][kFinishExperts], t_part[W];
+    const int n = a.x.vocab, blocks = static_cast<int>(gridDim.x);
     const int col = threadIdx.x % kFinishExperts, slice = threadIdx.x / kFinishExperts;
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     const int e = min(static_cast<int>(blockIdx.x) * kFinishExperts + col, n);
     double s = 0.0;
     int64_t c = 0, t = 0;
@@ -561,7 +716,7 @@ __global__ __launch_bounds__(kFinishThreads) void k_route_finish(RouteArgs a, Ro
             const int g = min(from + u * SLICES, w.groups - 1);
             v[u] = w.share[int64_t(g) * (n + 1) + e];
             k[u] = w.load[int64_t(g) * (n + 1) + e];
-            r[u] = w.load[int64_t(g) * (n + 1) + n];
+            r[u] = col == 0 ? w.load[int64_t(g) * (n + 1) + n] : 0;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -571,40 +726,51 @@ __global__ __launch_bounds__(kFinishThreads) void k_route_finish(RouteArgs a, Ro
             t += r[u];
         }
     }
-    s_part[slice][col] = s;
-    c_part[slice][col] = c;
-    if (col == 0) n_part[slice] = t;
+#pragma unroll
+    for (int d = kFinishExperts; d < kWave; d *= 2) {
+        s += __shfl_xor(s, d);
+        c += __shfl_xor(c, d);
+        t += __shfl_xor(t, d);
+    }
+    if (lane < kFinishExperts) {
+        s_part[wave][col] = s;
+        c_part[wave][col] = c;
+        if (col == 0) t_part[wave] = t;
+    }
     __syncthreads();
-    if (slice != 0 || static_cast<int>(blockIdx.x) * kFinishExperts + col > n) return;
+    if (threadIdx.x >= kWave) return;
     s = 0.0;
     c = t = 0;
-#pragma unroll 8
-    for (int i = 0; i < SLICES; ++i) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
         s += s_part[i][col];
         c += c_part[i][col];
-        t += n_part[i];
+        t += t_part[i];
     }
-    a.load[e] = c;
-    const double mean = t > 0 ? s / static_cast<double>(t) : 0.0;
-    if (e < n && a.share != nullptr) a.share[e] = static_cast<float>(mean);
-    if (e == n && a.aux != nullptr) a.aux[1] = static_cast<float>(mean);
-}
-
-__global__ __launch_bounds__(kRouteThreads) void k_route_aux(RouteArgs a)
-{
-    __shared__ double part[kRouteWaves];
-    const int n = a.x.vocab;
-    double s = 0.0;
-    for (int e = threadIdx.x; e < n; e += kRouteThreads)
-        s += static_cast<double>(a.load[e]) * static_cast<double>(a.share[e]);
-    s = lanes_sum<kWave>(s);
-    if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = s;
-    __syncthreads();
-    if (threadIdx.x != 0) return;
-    s = 0.0;
-    for (int i = 0; i < kRouteWaves; ++i) s += part[i];
-    const double tokens = static_cast<double>(a.load[n]);
-    a.aux[0] = tokens > 0.0 ? static_cast<float>(s * n / (a.top * tokens)) : 0.0f;
+    const bool mine = lane < kFinishExperts && static_cast<int>(blockIdx.x) * kFinishExperts + col <= n;
+    const double tokens = static_cast<double>(t), mean = t > 0 ? s / tokens : 0.0;
+    if (mine) {
+        a.load[e] = c;
+        if (e < n && a.share != nullptr) a.share[e] = static_cast<float>(mean);
+        if (e == n && a.aux != nullptr) a.aux[1] = static_cast<float>(mean);
+    }
+    if (a.aux == nullptr) return;
+    if (w.groups == 0) {
+        if (blockIdx.x == 0 && lane == 0) a.aux[0] = 0.0f;
+        return;
+    }
+    double part = lanes_sum<kWave>(mine && e < n ? static_cast<double>(c) * mean : 0.0);
+    int done = 0;
+    if (lane == 0) {
+        __hip_atomic_store(w.part + blockIdx.x, part, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        done = __hip_atomic_fetch_add(w.done, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    if (__builtin_amdgcn_readfirstlane(done) != blocks - 1) return;
+    part = 0.0;
+    for (int i = lane; i < blocks; i += kWave)
+        part += __hip_atomic_load(w.part + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    part = lanes_sum<kWave>(part);
+    if (lane == 0) a.aux[0] = t > 0 ? static_cast<float>(part * n / (a.top * tokens)) : 0.0f;
 }
 
 // With F the factor over the tokens routed, pull_e = F balance E load_e / (k N) and ds the gradient of
@@ -640,25 +806,26 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_grad(RouteGradArgs a)
         }
     }
     const double large = 2.0 * factor * static_cast<double>(a.large);
-    const int64_t step = int64_t(gridDim.x) * kRouteWaves * R;
-    for (int64_t first = (int64_t(blockIdx.x) * kRouteWaves + wave) * R; first < a.x.rows; first += step) {
-        const int64_t row = first + slot;
+    const int step = static_cast<int>(gridDim.x) * kRouteWaves * R;        // rows are below 2^22
+    for (int first = (static_cast<int>(blockIdx.x) * kRouteWaves + wave) * R; first < a.x.rows; first += step) {
+        int row = first + slot;
+        asm volatile("" : "+v"(row));       // addresses are formed from it, not each kept and stepped
         const bool in = row < a.x.rows;
         const bool live = in && (a.mask == nullptr || a.mask[row] != 0);
-        const T* x = static_cast<const T*>(a.x.x) + row * a.x.stride;
-        T* dx = static_cast<T*>(a.g.dx) + row * a.g.stride;
+        const T* x = static_cast<const T*>(a.x.x) + int64_t(row) * a.x.stride;
+        T* dx = static_cast<T*>(a.g.dx) + int64_t(row) * a.g.stride;
         int64_t id[U];
         float dw[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int i = u * L + sub;
-            id[u] = live && i < a.top ? a.ids[row * a.top + i] : -1;
-            dw[u] = a.dweights != nullptr && id[u] >= 0 ? a.dweights[row * a.top + i] * a.scale : 0.0f;
+            id[u] = live && i < a.top ? a.ids[int64_t(row) * a.top + i] : -1;
+            dw[u] = a.dweights != nullptr && id[u] >= 0 ? a.dweights[int64_t(row) * a.top + i] * a.scale : 0.0f;
         }
         float z[P];
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            if (live) load8<DT>(x, (c * L + sub) * 8, n, z + c * 8);
+            if (live) load8<DT>(x, (c * L + sub) * 8, n, -__builtin_inff(), z + c * 8);
             else
                 for (int j = 0; j < 8; ++j) z[c * 8 + j] = -__builtin_inff();
         }
@@ -672,8 +839,8 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_grad(RouteGradArgs a)
         }
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            bad |= z[i] != z[i];
             m = __builtin_fmaxf(m, z[i]);
+            if (i % 2 == 0) bad |= __builtin_isunordered(z[i], z[i + 1]);
         }
         m = lanes_max<L>(m);
         bad = lanes_max<L>(bad ? 1.0f : 0.0f) > 0.0f || (!SIGMOID && m == __builtin_inff());
@@ -682,7 +849,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_grad(RouteGradArgs a)
         float lane_sum = 0.0f;
         auto score = [](float v, float& u) {       // a sigmoid, and exp(-|v|) over 1 + that, squared
             const float t = exp2_hw(-__builtin_fabsf(v) * static_cast<float>(kLog2E));
-            const float r = 1.0f / (1.0f + t);
+            const float r = __builtin_amdgcn_rcpf(1.0f + t);
             u = t * r * r;
             return v >= 0.0f ? r : t * r;
         };
@@ -695,7 +862,8 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_grad(RouteGradArgs a)
         const double all = lanes_sum<L>(static_cast<double>(lane_sum));
         const bool nan = live && (bad || (!SIGMOID && !(all > 0.0)));
         const bool on = live && any && !nan;
-        const float part = all > 0.0 ? static_cast<float>(1.0 / all) : 0.0f;
+        const double inverse = all > 0.0 ? reciprocal(all) : 0.0;
+        const float part = static_cast<float>(inverse);
         // the chosen experts' scores and their gradient
         double ds[U];
         if (a.renormalise) {
@@ -711,10 +879,10 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_grad(RouteGradArgs a)
                 d += static_cast<double>(ws[u]);
                 mean += static_cast<double>(dw[u]) * static_cast<double>(ws[u]);
             }
-            d = lanes_sum<L>(d) + kTiny;
-            mean = lanes_sum<L>(mean) / d;
+            d = reciprocal(lanes_sum<L>(d) + kTiny);
+            mean = lanes_sum<L>(mean) * d;
 #pragma unroll
-            for (int u = 0; u < U; ++u) ds[u] = id[u] >= 0 ? (static_cast<double>(dw[u]) - mean) / d : 0.0;
+            for (int u = 0; u < U; ++u) ds[u] = id[u] >= 0 ? (static_cast<double>(dw[u]) - mean) * d : 0.0;
         } else {
 #pragma unroll
             for (int u = 0; u < U; ++u) ds[u] = static_cast<double>(dw[u]);
@@ -774,7 +942,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_grad(RouteGradArgs a)
         for (int u = 0; u < U; ++u)
             if (id[u] >= 0) extra[id[u]] = 0.0f;
         float base;
-        if constexpr (SIGMOID) base = all > 0.0 ? static_cast<float>(dot / all) : 0.0f;
+        if constexpr (SIGMOID) base = static_cast<float>(dot * inverse);
         else base = static_cast<float>((large != 0.0 ? large * (static_cast<double>(m) + log_sum(all)) : 0.0) - dot);
         const float off = nan ? __builtin_nanf("") : 0.0f;
 #pragma unroll
@@ -841,15 +1009,19 @@ int64_t route_grid(int64_t rows, int lanes, int64_t most)
 template <int DT, int L, int P, int K, bool EXACT>
 void route_shape(const RouteArgs& a, RouteSums& w, hipStream_t s)
 {
+    // with sums, as many workgroups as are resident at once: each leaves sums of its own
+    constexpr int64_t resident = 256 * route_waves<DT, P, EXACT>();
     int64_t most = 1 << 16;
     if (a.load != nullptr) {
-        most = MP_ROUTE_WORKSPACE_BYTES / (12 * (int64_t(a.x.vocab) + 1));
-        if (most > 1024) most = 1024;
+        most = (MP_ROUTE_WORKSPACE_BYTES - kFinishMost * 8 - 16) / (12 * (int64_t(a.x.vocab) + 1));
+        if (most > resident) most = resident;
     }
     const int64_t grid = route_grid(a.x.rows, L, most);
     if (a.load != nullptr) {
         w.groups = static_cast<int>(grid);
-        w.share = static_cast<double*>(a.workspace);
+        w.part = static_cast<double*>(a.workspace);
+        w.done = reinterpret_cast<int32_t*>(w.part + kFinishMost);
+        w.share = w.part + kFinishMost + 1;
         w.load = reinterpret_cast<int32_t*>(w.share + grid * (a.x.vocab + 1));
     }
     if (grid == 0) return;
@@ -884,7 +1056,7 @@ void route_dt(const RouteArgs& a, RouteSums& w, hipStream_t s)
 template <int DT, int L, int P>
 void grad_shape(const RouteGradArgs& a, hipStream_t s)
 {
-    const unsigned grid = static_cast<unsigned>(route_grid(a.x.rows, L, 4096));
+    const unsigned grid = static_cast<unsigned>(route_grid(a.x.rows, L, 1024));
     if (a.sigmoid) k_route_grad<DT, L, P, true><<<grid, kRouteThreads, 0, s>>>(a);
     else k_route_grad<DT, L, P, false><<<grid, kRouteThreads, 0, s>>>(a);
 }
@@ -910,7 +1082,6 @@ hipError_t launch_route(const RouteArgs& a, int dtype, hipStream_t s)
     if (a.load != nullptr) {
         const unsigned cols = static_cast<unsigned>(a.x.vocab) / kFinishExperts + 1;
         k_route_finish<<<cols, kFinishThreads, 0, s>>>(a, w);
-        if (a.aux != nullptr) k_route_aux<<<1, kRouteThreads, 0, s>>>(a);
     }
     return hipGetLastError();
 }

@@ -7,7 +7,8 @@ A chosen expert's own exponential is binary64's.  What is summed over the expert
 the shares) may be fp32 with a relative error of E = 4 u (|z| + 2), z the logit (softmax: its difference
 to the largest), u = 2^-24: an exponent of two roundings of its size, an exponential good to one step; so
 is the gradient, formed in fp32.  A sum over a token's experts is then off by the mean of E over the
-shares, a share by that, its own E and four roundings; a weight that is not divided by the chosen
+shares, a share by that, its own E and four roundings, and the sum over the tokens by a rounding for
+each 4096 tokens (a lane's own additions, the lanes' are joined in binary64); a weight that is not divided by the chosen
 ones' sum by the softmax's sum.
 """
 import numpy as np
@@ -84,7 +85,7 @@ def route(x, bias, mask, sigmoid, top, groups=1, top_groups=1, best=1, renormali
     with np.errstate(all="ignore"):
         sum_off = np.nan_to_num((s * E).sum(1) / s.sum(1)) + 2 * U
     off_w = np.abs(w) * (1e-13 if sigmoid or renormalise else sum_off[:, None])
-    off_p = (p * (E[ok] + sum_off[ok][:, None] + 4 * U)).sum(0) / tokens if len(p) else 0.0 * share
+    off_p = (p * (E[ok] + sum_off[ok][:, None] + (4 + rows // 4096) * U)).sum(0) / tokens if len(p) else 0.0 * share
     off_lse = (2 * np.abs(lse[ok]) * (sum_off[ok] + 2 * U)).sum() / tokens if not sigmoid else 0.0
     return dict(ids=ids, weights=w, load=load, share=share, aux=aux,
                 tol_weights=round_tol(w) + off_w, tol_share=round_tol(share) + off_p,
