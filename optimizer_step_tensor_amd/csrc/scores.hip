@@ -18,6 +18,8 @@
 // operations a logit, and its exponential counts for four of them.
 #include <float.h>
 
+#include <algorithm>
+
 #include "rows.h"
 #include "scores.h"
 
@@ -334,6 +336,10 @@ __device__ __forceinline__ void put_key(Lists<THREADS>& l, uint64_t key)
     if (i < Lists<THREADS>::kKeys) l.key[i] = key;
 }
 
+// -inf in 32 bits of a vector.
+template <int DT>
+constexpr uint32_t kGoneBits = DT == kBF16 ? 0xFF80FF80u : DT == kFP16 ? 0xFC00FC00u : 0xFF800000u;
+
 // Shares of a piece's vectors, and with TOP the slots; `per` pairs to a slot.
 template <int DT, int THREADS, bool TOP, bool NT>
 __device__ __forceinline__ void piece_sums(Share& share, const Piece<DT>& p, const RowScale& k,
@@ -363,17 +369,39 @@ __device__ __forceinline__ void piece_sums(Share& share, const Piece<DT>& p, con
         for (int u = 0; u < U; u += 2) pair(v[u], v[u + 1]);
     }
     for (; base < p.hi; base += 2 * THREADS) {
-        constexpr uint32_t gone = DT == kBF16 ? 0xFF80FF80u : DT == kFP16 ? 0xFC00FC00u : 0xFF800000u;     // -inf
         const int i = base + tid, j = i + THREADS;
         u32x4 a = load_vec<DT, NT>(p.at(min(i, p.hi - 1)));
         u32x4 b = load_vec<DT, NT>(p.at(min(j, p.hi - 1)));
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            if (i >= p.hi) a[e] = gone;
-            if (j >= p.hi) b[e] = gone;
+            if (i >= p.hi) a[e] = kGoneBits<DT>;
+            if (j >= p.hi) b[e] = kGoneBits<DT>;
         }
         pair(a, b);
     }
+}
+
+// The largest of a wave's.
+template <class N, int D = 1>
+__device__ __forceinline__ N lanes_largest(N v)
+{
+    if constexpr (D < kWave) {
+        uint32_t a0, b0, a1 = 0, b1 = 0;
+        N a, b;
+        if constexpr (sizeof(N) == 8) {
+            const uint64_t u = __builtin_bit_cast(uint64_t, v);
+            across<D>(static_cast<uint32_t>(u), a0, b0);
+            across<D>(static_cast<uint32_t>(u >> 32), a1, b1);
+            a = __builtin_bit_cast(N, uint64_t(a1) << 32 | a0);
+            b = __builtin_bit_cast(N, uint64_t(b1) << 32 | b0);
+        } else {
+            across<D>(__builtin_bit_cast(uint32_t, v), a0, b0);
+            a = __builtin_bit_cast(N, a0);
+            b = __builtin_bit_cast(N, b0);
+        }
+        return lanes_largest<N, 2 * D>(a > b ? a : b);
+    }
+    return v;
 }
 
 // A bound on the order that at least k of the workgroup's lane maxima reach and not many more: found
@@ -389,13 +417,8 @@ __device__ __forceinline__ uint32_t lane_bound(const Lists<THREADS>& l, int k)
         lo = min(lo, v[i]);
         hi = max(hi, v[i]);
     }
-#pragma unroll
-    for (int d = 1; d < kWave; d *= 2) {
-        lo = min(lo, static_cast<uint32_t>(__shfl_xor(static_cast<int>(lo), d)));
-        hi = max(hi, static_cast<uint32_t>(__shfl_xor(static_cast<int>(hi), d)));
-    }
-    lo = __builtin_amdgcn_readfirstlane(lo);
-    hi = __builtin_amdgcn_readfirstlane(hi);
+    lo = ~__builtin_amdgcn_readfirstlane(lanes_largest(~lo));
+    hi = __builtin_amdgcn_readfirstlane(lanes_largest(hi));
     int bit = 31 - __builtin_clz((lo ^ hi) | 1);
     uint32_t bound = hi >> bit >> 1 << bit << 1;              // what all have in common
     for (; bit >= 0; --bit) {
@@ -482,14 +505,14 @@ __device__ __forceinline__ void emit_ranked(const Lists<THREADS>& l, int n, int 
     for (int i = n + static_cast<int>(threadIdx.x); i < k; i += THREADS) emit(i, uint64_t(0));
 }
 
-template <int DT, int THREADS, class F>
-__device__ __forceinline__ void choose(const Piece<DT>& p, float lane_max, int per, int k, Lists<THREADS>& l,
+// The k largest of a piece: collect(bound) puts all keys that reach the bound and ends with a barrier;
+// false where there are too many.
+template <int DT, int THREADS, class C, class F>
+__device__ __forceinline__ void choose(const Piece<DT>& p, float lane_max, int k, Lists<THREADS>& l, C collect,
                                        F emit)
 {
-    constexpr int E = Fmt<DT>::E;
     const int tid = threadIdx.x;
-    const uint32_t own = order_of(lane_max);
-    l.lane_max[tid] = own;
+    l.lane_max[tid] = order_of(lane_max);
     if (tid == 0) l.lanes = l.hits = l.keys = 0;
     __syncthreads();
     if (tid < kWave) {
@@ -497,9 +520,18 @@ __device__ __forceinline__ void choose(const Piece<DT>& p, float lane_max, int p
         if (tid == 0) l.bound = b;
     }
     __syncthreads();
-    const uint32_t bound = l.bound;
-    const float least = order_value(bound);
-    if (own >= bound) l.lane[atomicAdd(&l.lanes, 1)] = static_cast<uint16_t>(tid);
+    const bool fits = collect(l.bound);
+    if (!fits || l.keys > Lists<THREADS>::kKeys) choose_by_passes(p, k, l);
+    emit_ranked(l, l.keys, k, emit);
+}
+
+// The keys of a piece whose slots say where they are.
+template <int DT, int THREADS>
+__device__ __forceinline__ bool collect_by_slots(const Piece<DT>& p, uint32_t bound, int per, Lists<THREADS>& l)
+{
+    constexpr int E = Fmt<DT>::E;
+    const int tid = threadIdx.x;
+    if (l.lane_max[tid] >= bound) l.lane[atomicAdd(&l.lanes, 1)] = static_cast<uint16_t>(tid);
     __syncthreads();
     const int pairs = (p.hi - p.lo + 2 * THREADS - 1) / (2 * THREADS);
     const int slots = (pairs + per - 1) / per;
@@ -514,23 +546,22 @@ __device__ __forceinline__ void choose(const Piece<DT>& p, float lane_max, int p
         }
     __syncthreads();                          // from here on keys take the slots' place
     const int hits = l.hits;
-    if (hits <= Lists<THREADS>::kHits) {
-        const int each = 2 * per;
-        for (int i = tid; i < hits * each; i += THREADS) {
-            const int h = l.hit[i / each];
-            const int vec = p.lo + (h / THREADS * each + i % each) * THREADS + h % THREADS;
-            if (vec >= p.hi) continue;
-            float v[E];
-            unpack<DT>(load_vec<DT, false>(p.at(vec)), v);
+    if (hits > Lists<THREADS>::kHits) return false;
+    const float least = order_value(bound);
+    const int each = 2 * per;
+    for (int i = tid; i < hits * each; i += THREADS) {
+        const int h = l.hit[i / each];
+        const int vec = p.lo + (h / THREADS * each + i % each) * THREADS + h % THREADS;
+        if (vec >= p.hi) continue;
+        float v[E];
+        unpack<DT>(load_vec<DT, false>(p.at(vec)), v);
 #pragma unroll
-            for (int j = 0; j < E; ++j)
-                if (v[j] >= least) put_key(l, entry_key(v[j], p.head + vec * E + j));
-        }
-        if (p.one >= 0 && p.single >= least) put_key(l, entry_key(p.single, p.one));
-        __syncthreads();
+        for (int j = 0; j < E; ++j)
+            if (v[j] >= least) put_key(l, entry_key(v[j], p.head + vec * E + j));
     }
-    if (hits > Lists<THREADS>::kHits || l.keys > Lists<THREADS>::kKeys) choose_by_passes(p, k, l);
-    emit_ranked(l, l.keys, k, emit);
+    if (p.one >= 0 && p.single >= least) put_key(l, entry_key(p.single, p.one));
+    __syncthreads();
+    return true;
 }
 
 // The sums of a piece, relative to 2^ref (in the first wave; m in all lanes).
@@ -539,13 +570,11 @@ struct PieceStat {
     float m;
 };
 
-template <int DT, int THREADS, bool TOP>
-__device__ __forceinline__ PieceStat piece_stat(const Piece<DT>& p, const RowScale& k, bool stream, int per,
-                                                Lists<THREADS>& l, JoinSpace<THREADS>& space, float& lane_max)
+// From the lanes' shares of a piece's vectors.
+template <int DT, int THREADS>
+__device__ __forceinline__ PieceStat piece_stat(Share share, const Piece<DT>& p, const RowScale& k,
+                                                JoinSpace<THREADS>& space, float& lane_max)
 {
-    Share share;
-    if (stream) piece_sums<DT, THREADS, TOP, true>(share, p, k, l, per);
-    else piece_sums<DT, THREADS, TOP, false>(share, p, k, l, per);
     if (p.one >= 0) add_one(share, p.single, k.k, k.slack);
     lane_max = share.m;
     PieceStat r;
@@ -623,7 +652,10 @@ __global__ __launch_bounds__(THREADS, 8) void k_scores(ScoreArgs a, int per)
     const float xt = target < n ? widen<DT>(x[target]) : 0.0f;
     float lane_max;
     auto& l = reinterpret_cast<Lists<THREADS>&>(lists);
-    const PieceStat st = piece_stat<DT, THREADS, TOP>(p, k, a.x.stream, per, l, space, lane_max);
+    Share share;
+    if (a.x.stream) piece_sums<DT, THREADS, TOP, true>(share, p, k, l, per);
+    else piece_sums<DT, THREADS, TOP, false>(share, p, k, l, per);
+    const PieceStat st = piece_stat<DT, THREADS>(share, p, k, space, lane_max);
     __shared__ RowStat whole;
     if (threadIdx.x < kWave) {
         const RowStat r = stat_of(st.m, st.ref, st.s, st.c, k);
@@ -633,14 +665,16 @@ __global__ __launch_bounds__(THREADS, 8) void k_scores(ScoreArgs a, int per)
         }
     }
     if constexpr (TOP)
-        choose<DT, THREADS>(p, lane_max, per, a.top, l, [&](int rank, uint64_t key) {
-            write_entry(a, row * a.top + rank, key, whole);
-        });
+        choose<DT, THREADS>(
+            p, lane_max, a.top, l, [&](uint32_t bound) { return collect_by_slots(p, bound, per, l); },
+            [&](int rank, uint64_t key) { write_entry(a, row * a.top + rank, key, whole); });
 }
 
 // Few rows, less than the chip has room for: a row is cut into parts, one workgroup each, that leave
-// their sums and their own k largest in the workspace; then one workgroup a row joins them.
+// their sums and their own k largest in the workspace; then one workgroup a row joins them.  A lane
+// holds its vectors of a part, up to kPartHeld: the choice needs no slots and no second read then.
 constexpr int kPartThreads = 256;
+constexpr int kPartHeld = 4;
 constexpr int kMaxParts = kWave;
 
 struct ScoreParts {
@@ -649,7 +683,7 @@ struct ScoreParts {
     int parts, vecs;         // per row; vectors of a part
 };
 
-template <int DT, bool TOP>
+template <int DT, bool TOP, bool HELD>
 __global__ __launch_bounds__(kPartThreads) void k_score_parts(ScoreArgs a, ScoreParts w, int per)
 {
     using T = typename Fmt<DT>::T;
@@ -671,12 +705,47 @@ __global__ __launch_bounds__(kPartThreads) void k_score_parts(ScoreArgs a, Score
     p.single = p.one >= 0 ? widen<DT>(x[p.one]) : 0.0f;
     float lane_max;
     auto& l = reinterpret_cast<Lists<kPartThreads>&>(lists);
-    const PieceStat st = piece_stat<DT, kPartThreads, TOP>(p, k, false, per, l, space, lane_max);
+    Share share;
+    u32x4 v[kPartHeld];
+    if constexpr (HELD) {
+#pragma unroll
+        for (int u = 0; u < kPartHeld; ++u)
+            v[u] = load_vec<DT, false>(p.at(max(min(p.lo + u * kPartThreads + static_cast<int>(threadIdx.x), p.hi - 1), 0)));
+#pragma unroll
+        for (int u = 0; u < kPartHeld; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (p.lo + u * kPartThreads + static_cast<int>(threadIdx.x) >= p.hi) v[u][e] = kGoneBits<DT>;
+#pragma unroll
+        for (int u = 0; u < kPartHeld; u += 2) add_pair<DT>(share, v[u], v[u + 1], k);
+    } else {
+        piece_sums<DT, kPartThreads, TOP, false>(share, p, k, l, per);
+    }
+    const PieceStat st = piece_stat<DT, kPartThreads>(share, p, k, space, lane_max);
     if (threadIdx.x == 0) w.stat[blockIdx.x] = st;
     if constexpr (TOP)
-        choose<DT, kPartThreads>(p, lane_max, per, a.top, l, [&](int rank, uint64_t key) {
-            w.key[int64_t(blockIdx.x) * a.top + rank] = key;
-        });
+        choose<DT, kPartThreads>(
+            p, lane_max, a.top, l,
+            [&](uint32_t bound) {
+                if constexpr (!HELD) return collect_by_slots(p, bound, per, l);
+                constexpr int E = Fmt<DT>::E;
+                const float least = order_value(bound);
+                if (lane_max >= least) {
+#pragma unroll
+                    for (int u = 0; u < kPartHeld; ++u) {
+                        float f[E];
+                        unpack<DT>(v[u], f);
+#pragma unroll
+                        for (int j = 0; j < E; ++j)
+                            if (f[j] >= least)
+                                put_key(l, entry_key(f[j], p.head + (p.lo + u * kPartThreads + static_cast<int>(threadIdx.x)) * E + j));
+                    }
+                    if (p.one >= 0 && p.single >= least) put_key(l, entry_key(p.single, p.one));
+                }
+                __syncthreads();
+                return true;
+            },
+            [&](int rank, uint64_t key) { w.key[int64_t(blockIdx.x) * a.top + rank] = key; });
 }
 
 template <int DT, bool TOP>
@@ -696,10 +765,11 @@ __global__ __launch_bounds__(kPartThreads) void k_score_join(ScoreArgs a, ScoreP
     if (lane < w.parts) st = w.stat[row * w.parts + lane];
     constexpr int kEach = Lists<kPartThreads>::kKeys / kPartThreads;
     const int entries = w.parts * a.top;                   // at most kKeys
-    uint64_t key[TOP ? kEach : 1], bound = ~uint64_t(0);
+    uint64_t key[TOP ? kEach : 1], bound = 0;
     if constexpr (TOP) {
         const uint64_t* list = w.key + row * entries;
-        // of P sorted lists the k / P-th entries: at least k entries reach the smallest of them
+        // of P sorted lists the entries d + 1 deep, d + 1 = k / P rounded up: at least k entries reach the
+        // j-th largest of these, j = k / (d + 1) rounded up
         const int deep = (a.top + w.parts - 1) / w.parts - 1;
         if (lane < w.parts) bound = list[lane * a.top + deep];
 #pragma unroll
@@ -707,13 +777,8 @@ __global__ __launch_bounds__(kPartThreads) void k_score_join(ScoreArgs a, ScoreP
     }
     const float m = lanes_max<kWave>(st.m);
     // a part without any element in reach has no say in the reference; a NaN's is kept
-    double ref = st.s != 0.0 ? st.ref : -__builtin_inf();
     const double own = st.ref;
-#pragma unroll
-    for (int d = 1; d < kWave; d *= 2) {
-        const double o = __shfl_xor(ref, d);
-        ref = o > ref ? o : ref;
-    }
+    const double ref = lanes_largest(st.s != 0.0 ? own : -__builtin_inf());
     const double d = st.s != 0.0 ? own - ref : 0.0;
     const double down = static_cast<double>(exp2_hw(static_cast<float>(d)));
     const double c = lanes_sum<kWave>(down == 0.0 ? 0.0 : (st.c + st.s * d) * down);
@@ -722,12 +787,18 @@ __global__ __launch_bounds__(kPartThreads) void k_score_join(ScoreArgs a, ScoreP
     if (tid == 0) write_row(a, row, target, xt, r);
     if constexpr (TOP) {
         auto& l = reinterpret_cast<Lists<kPartThreads>&>(lists);
-#pragma unroll
-        for (int e = 1; e < kWave; e *= 2) {
-            const uint64_t o = __shfl_xor(bound, e);
-            bound = o < bound ? o : bound;
-        }
-        if (bound == 0) bound = 1;                     // an empty place is no entry
+        const int deep = (a.top + w.parts - 1) / w.parts, nth = (a.top + deep - 1) / deep;
+        const double b = __builtin_bit_cast(double, bound);       // a positive number, as in emit_ranked
+        auto of_lane = [&](int i) {
+            const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(bound), i);
+            const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(bound >> 32), i);
+            return uint64_t(hi) << 32 | lo;
+        };
+        int before = 0;
+        for (int i = 0; i < w.parts; ++i) before += __builtin_bit_cast(double, of_lane(i)) > b;
+        // of keys none is alike; where the j-th is an empty place, all keys are taken
+        const uint64_t nth_lane = __builtin_amdgcn_ballot_w64(lane < w.parts && before == nth - 1 && bound != 0);
+        bound = nth_lane != 0 ? of_lane(__builtin_ctzll(nth_lane)) : 1;
         if (tid == 0) l.keys = 0;
         __syncthreads();
 #pragma unroll
@@ -837,28 +908,32 @@ void whole_rows(const ScoreArgs& a, hipStream_t s)
     else k_scores<DT, THREADS, false><<<rows, THREADS, 0, s>>>(a, per);
 }
 
+// Rows of at least kSplitVecs vectors, up to kSplitRows of them.  A call, 20 entries, split against whole:
+// 128256 bf16 logits (16032 vectors), 1 row 15.1 us against 18.5, 64 rows 17.2 against 22.8, 128
+// rows 22.4 against 23.8, 200 rows 27.3 against 24.4; 60000 fp32 logits (15000), 1 row 13.4 against 15.5, 128
+// rows 18.3 against 23.4, 300 rows 27.1 against 25.1; 50304 bf16 logits (6288), 1 row 12.9 against 11.4.
 constexpr int kSplitRows = 128;
-constexpr int kSplitVocab = 16 * 1024;
+constexpr int kSplitVecs = 10000;
 
 // Split the rows over several workgroups?  Fills `w` in the workspace if so.
 template <int DT>
 bool split(const ScoreArgs& a, ScoreParts* w)
 {
-    if (a.workspace == nullptr || a.x.rows > kSplitRows || a.x.vocab < kSplitVocab) return false;
     const int nvec = a.x.vocab / Fmt<DT>::E;
-    int parts = 512 / a.x.rows;
-    if (parts > kMaxParts) parts = kMaxParts;
-    if (a.top > 0 && parts > Lists<kPartThreads>::kKeys / a.top) parts = Lists<kPartThreads>::kKeys / a.top;
-    const int most = (nvec + 2 * kPartThreads - 1) / (2 * kPartThreads);
-    if (parts > most) parts = most;
+    if (a.workspace == nullptr || a.x.rows > kSplitRows || nvec < kSplitVecs) return false;
+    const int entry = static_cast<int>(sizeof(PieceStat)) + 8 * a.top;
+    // what the joining workgroup and the workspace have room for
+    int most = a.top > 0 ? std::min(kMaxParts, Lists<kPartThreads>::kKeys / a.top) : kMaxParts;
+    most = static_cast<int>(std::min<int64_t>(most, MP_SCORE_WORKSPACE_BYTES / (int64_t(entry) * a.x.rows)));
+    // two workgroups for each compute unit, parts of two vectors a lane at least, and such as lanes can
+    // hold if possible
+    int parts = std::min(512 / a.x.rows, (nvec + 2 * kPartThreads - 1) / (2 * kPartThreads));
+    parts = std::min(std::max(parts, (nvec + kPartHeld * kPartThreads - 1) / (kPartHeld * kPartThreads)), most);
     if (parts < 2) return false;
     w->vecs = (nvec + parts - 1) / parts;
     w->parts = (nvec + w->vecs - 1) / w->vecs;
-    const int64_t pieces = int64_t(a.x.rows) * w->parts;
-    const size_t stats = sizeof(PieceStat) * pieces;
-    if (stats + sizeof(uint64_t) * pieces * a.top > MP_SCORE_WORKSPACE_BYTES) return false;
     w->stat = static_cast<PieceStat*>(a.workspace);
-    w->key = reinterpret_cast<uint64_t*>(static_cast<char*>(a.workspace) + stats);
+    w->key = reinterpret_cast<uint64_t*>(w->stat + int64_t(a.x.rows) * w->parts);
     return true;
 }
 
@@ -870,11 +945,14 @@ void scores_dt(ScoreArgs a, hipStream_t s)
     if (split<DT>(a, &w)) {
         const unsigned rows = static_cast<unsigned>(a.x.rows), all = rows * static_cast<unsigned>(w.parts);
         const int per = pairs_per_slot<kPartThreads>(w.vecs);
+        const bool held = w.vecs <= kPartHeld * kPartThreads;
         if (a.top > 0) {
-            k_score_parts<DT, true><<<all, kPartThreads, 0, s>>>(a, w, per);
+            if (held) k_score_parts<DT, true, true><<<all, kPartThreads, 0, s>>>(a, w, per);
+            else k_score_parts<DT, true, false><<<all, kPartThreads, 0, s>>>(a, w, per);
             k_score_join<DT, true><<<rows, kPartThreads, 0, s>>>(a, w);
         } else {
-            k_score_parts<DT, false><<<all, kPartThreads, 0, s>>>(a, w, per);
+            if (held) k_score_parts<DT, false, true><<<all, kPartThreads, 0, s>>>(a, w, per);
+            else k_score_parts<DT, false, false><<<all, kPartThreads, 0, s>>>(a, w, per);
             k_score_join<DT, false><<<rows, kPartThreads, 0, s>>>(a, w);
         }
         return;
