@@ -957,9 +957,15 @@ void scores_dt(ScoreArgs a, hipStream_t s)
         }
         return;
     }
+    // Workgroups of 256 lanes; of fewer for short rows, whose joins and barriers would cost more than
+    // their logits, and for somewhat longer ones where there are enough of them to fill the chip.  bf16, 20
+    // entries, 64, 128 and 256 lanes: 8192 x 2000 23, 25 and 40 us, 8192 x 8192 38, 38 and 45, 8192 x 16000
+    // 68, 61 and 66, 8192 x 64000 197, 181 and 179; 512 x 8192 11.0, 9.6 and 9.8, 512 x 32000 24, 18 and 14.
+    // (A bound from 64 lanes' maxima is one for at most 64 entries.)
     const int nvec = a.x.vocab / Fmt<DT>::E;
-    // a bound from 64 lanes' maxima is one for at most 64 entries
-    if (nvec <= 64 * 8 && a.top <= 64) whole_rows<DT, 64>(a, s);
+    const bool many = a.x.rows >= 2048;
+    if (nvec <= (many ? 1024 : 512) && a.top <= 64) whole_rows<DT, 64>(a, s);
+    else if (nvec <= (many ? 4096 : 512)) whole_rows<DT, 128>(a, s);
     else whole_rows<DT, 256>(a, s);
 }
 
