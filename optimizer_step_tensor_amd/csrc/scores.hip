@@ -899,13 +899,19 @@ int pairs_per_slot(int vecs)
     return per > 0 ? per : 1;
 }
 
+// Without lists, five workgroups of 256 lanes on a compute unit (this much shared memory each, unused):
+// with eight, 2048 rows would all be there at once, and where a third of them is switched off
+// some units would have eight live ones and others three.  2048 x 128256 bf16, 0.3 off, 68 us
+// against 74; 8192 x 128256 287 either way, 4096 x 50304 65.
+constexpr unsigned kReserved = 32000;
+
 template <int DT, int THREADS>
 void whole_rows(const ScoreArgs& a, hipStream_t s)
 {
     const unsigned rows = static_cast<unsigned>(a.x.rows);
     const int per = pairs_per_slot<THREADS>(a.x.vocab / Fmt<DT>::E);
     if (a.top > 0) k_scores<DT, THREADS, true><<<rows, THREADS, 0, s>>>(a, per);
-    else k_scores<DT, THREADS, false><<<rows, THREADS, 0, s>>>(a, per);
+    else k_scores<DT, THREADS, false><<<rows, THREADS, THREADS == 256 ? kReserved : 0, s>>>(a, per);
 }
 
 // Rows of at least kSplitVecs vectors, up to kSplitRows of them.  A call, 20 entries, split against whole:

@@ -120,6 +120,29 @@ def test_rows(mp, rows):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("vectors,top", [(1000, 7), (1030, 65), (1700, 20), (1700, 0), (4100, 9)])
+def test_many_rows(mp, kind, vectors, top):
+    """Rows of which workgroups of 64, 128 and 256 lanes are taken, where there are many: 2100 that
+    repeat 20."""
+    V = vectors * (4 if kind == "fp32" else 8) + 3
+    x, t = make_x(gen(18, V), 20, V, kind)
+    t = np.where(np.arange(20) % 5 == 3, -100, t)
+    T = float(np.float32(0.9))
+    want = ref.score(x, t, T, top)
+    b = Buf(2100, V, kind, init=np.resize(x, (2100, V)))
+    o = Out(mp, 2100, top)
+    mp.mp_token_score(mp.logits(b.t, T), dev(np.resize(t, 2100)), o.struct)
+    for name in ("logp", "lse", "entropy"):
+        check(name, getattr(o, name), np.resize(held(want[name]), 2100), np.resize(want["tol_" + name], 2100))
+    if top:
+        assert np.array_equal(o.top_ids.cpu().numpy(), np.resize(want["ids"], (2100, top)))
+        assert np.array_equal(host(o.top_values), np.resize(want["values"], (2100, top)))
+        check("top_logp", o.top_logp, np.resize(held(want["top_logp"]), (2100, top)),
+              np.resize(want["tol_top_logp"], (2100, top)))
+    assert o.untouched() and b.untouched()
+
+
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("V,top", [(40, 64), (5000, 50), (70001, 128)])
 def test_equal_logits_come_in_the_order_of_their_ids(mp, kind, V, top):
     import torch

@@ -235,4 +235,4 @@ def test_no_scratch_and_bounded_vgprs(tmp_path):
     assert len(found) >= 8
     for name, body in found:
         assert int(re.search(r"private_segment_fixed_size (\d+)", body).group(1)) == 0, name
-        assert int(re.search(r"next_free_vgpr (\d+)", body).group(1)) <= 512, name
+        assert int(re.search(r"next_free_vgpr (\d+)", body).group(1)) <= 256, name
