@@ -15,6 +15,7 @@
 // experts do the least: a join costs the same however many lanes repeat it.
 #include <float.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "rows.h"
@@ -132,21 +133,36 @@ __device__ __forceinline__ double key_of(double c, int e)
     return __builtin_bit_cast(double, uint64_t(hi) << 32 | ((static_cast<uint32_t>(u) & ~mask) | last));
 }
 
-template <class Key, bool EXACT>
+// 16-bit logits: the order in a key's upper half, the expert in its lower one.  Two of a word are put in
+// order at a time, -0 as 0; `size` becomes the largest magnitudes, above an infinity's where there is a NaN.
+typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
+template <int DT>
+constexpr uint32_t kInfBits = DT == kBF16 ? 0x7F80u : 0x7C00u;
+
+__device__ __forceinline__ uint32_t order_of_pair(uint32_t w, u16x2& size)
+{
+    const i16x2 sign = __builtin_bit_cast(i16x2, w) >> i16x2{15, 15};
+    const i16x2 most = __builtin_bit_cast(i16x2, w & 0x7FFF7FFFu);
+    size = __builtin_elementwise_max(size, __builtin_bit_cast(u16x2, most));
+    const i16x2 k = (most ^ sign) - sign;
+    return __builtin_bit_cast(uint32_t, k) ^ 0x80008000u;
+}
+
+template <int DT>
+__device__ __forceinline__ float logit_of_key(uint32_t key)
+{
+    const uint32_t o = key >> 16;
+    return widen<DT>(static_cast<uint16_t>(o & 0x8000u ? o ^ 0x8000u : 0x10000u - o));
+}
+
+template <int DT, class Key, bool EXACT>
 __device__ __forceinline__ bool is_open(Key key)
 {
     if constexpr (EXACT) return key > kOpen;
-    else return key > no_key<Key>();
-}
-
-// A 16-bit logit's order in the upper half (never 0: -inf has no key).
-template <int DT>
-__device__ __forceinline__ uint32_t key_of_logit(float z, int e)
-{
-    const float f = z + 0.0f;
-    const uint32_t h = DT == kBF16 ? __float_as_uint(f) >> 16
-                                   : __builtin_bit_cast(uint16_t, static_cast<_Float16>(f));
-    return (h & 0x8000u ? 0xFFFFu - h : h + 0x8000u) << 16 | (0xFFFFu - static_cast<uint32_t>(e));
+    else if constexpr (DT == kFP32) return key > no_key<Key>();
+    else return key > ((0x8000u - kInfBits<DT>) << 16 | 0xFFFFu);          // -inf and none
 }
 
 template <class Key>
@@ -229,6 +245,13 @@ __device__ __forceinline__ Key partner(Key v)
     }
 }
 
+template <int L, int D = 1, class Key>
+__device__ __forceinline__ Key largest_key(Key v)
+{
+    if constexpr (D < L) return largest_key<L, 2 * D>(max_key(v, partner<D>(v)));
+    return v;
+}
+
 // The K best of two sorted lists, the other one a lane's D away.
 template <int D, int K, class Key>
 __device__ __forceinline__ void join_lists(Key (&k)[K])
@@ -296,6 +319,19 @@ __device__ __forceinline__ void load8(const typename Fmt<DT>::T* x, int e, int n
     }
 }
 
+// The same of 16-bit logits as they are.
+template <int DT>
+__device__ __forceinline__ u32x4 load8_raw(const uint16_t* x, int e, int n)
+{
+    if (e + 8 <= n) return load_vec<DT, false>(x + e);
+    constexpr uint32_t gone = 0x8000u | kInfBits<DT>;
+    const int end = here(n);
+    uint32_t h[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] = e + j < end ? x[e + j] : gone;
+    return u32x4{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
+}
+
 // The waves of a workgroup share nothing but counts: what a wave writes to its own part of the shared
 // memory its lanes read back in order.
 __device__ __forceinline__ void wave_fence()
@@ -318,12 +354,18 @@ __host__ __device__ __forceinline__ int group_keys(int n, int groups, int all)
 }
 
 // L lanes per token, P experts a lane: expert (c L + lane) 8 + j is the lane's P's c 8 + j.
+// Bound by the vector units.  131072 x 128 bf16, 8 of 128 by logits: 23.5 us, 93 of 100 cycles of them, 43
+// instructions an expert and lane with the sorting, against 7 us for reads and writes.  65536 x 256 bf16,
+// 8 of 256 by a bias in 4 of 8 groups, with sums: 58 us, 82 instructions of which the binary64
+// score is 32; two waves a SIMD, all that 16 experts' keys leave room for, keep the units at work
+// two thirds of the time.  7 x 64: 3.2 us, a launch.
 template <int DT, int L, int P, int K, bool EXACT>
 __global__ __launch_bounds__(kRouteThreads, (route_waves<DT, P, EXACT>())) void k_route(RouteArgs a, RouteSums w, int space_bytes)
 {
     using T = typename Fmt<DT>::T;
     using Key = std::conditional_t<EXACT || DT == kFP32, double, uint32_t>;
     constexpr int R = kWave / L, C = P / 8, N = L * P;         // tokens a wave, chunks a lane, experts
+    constexpr bool PACKED = std::is_same_v<Key, uint32_t>;
     extern __shared__ __align__(16) char space[];       // a part for each wave
     __shared__ int32_t count[N];
     __shared__ __align__(16) float bias_of[EXACT ? N : 1];
@@ -342,8 +384,9 @@ __global__ __launch_bounds__(kRouteThreads, (route_waves<DT, P, EXACT>())) void 
     Key* const group_of = mine + keys;
     uint8_t* const open_of = reinterpret_cast<uint8_t*>(reinterpret_cast<Key*>(own_space) + R * (keys + a.groups)) +
                              slot * a.groups;
-    // A lane's sums are of at most some hundred tokens, fp32 (binary64 ones would take sixteen registers
-    // more than there are for three waves a SIMD); the lanes' are joined in binary64.
+    // A lane's sums are fp32, of 2^22 tokens over at least 1364 waves (binary64 ones would take sixteen registers
+    // more than there are for three waves a SIMD): below 3100 additions, 2^-12.4 relative if all of them
+    // were off the same way.  The lanes' are joined in binary64.
     float total[P] = {};
     double squares = 0.0;
     int tokens = 0;
@@ -373,21 +416,44 @@ __global__ __launch_bounds__(kRouteThreads, (route_waves<DT, P, EXACT>())) void 
         asm volatile("" : "+v"(row));       // addresses are formed from it, not each kept and stepped
         const bool live = row < a.x.rows && (a.mask == nullptr || a.mask[row] != 0);
         const T* x = static_cast<const T*>(a.x.x) + int64_t(row) * a.x.stride;
-        float z[P];
+        Key key[P];
+        bool bad = false, tame = false;
+        float m;
+        u32x4 raw[PACKED ? C : 1];
+        float z[PACKED ? 1 : P];
+        if constexpr (PACKED) {
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            if (live) load8<DT>(x, (c * L + sub) * 8, n, EXACT ? -kTame : -__builtin_inff(), z + c * 8);
-            else
-                for (int j = 0; j < 8; ++j) z[c * 8 + j] = 0.0f;
+            for (int c = 0; c < C; ++c)
+                raw[c] = live ? load8_raw<DT>(x, (c * L + sub) * 8, n) : u32x4{0u, 0u, 0u, 0u};
+            u16x2 size = {0, 0};
+#pragma unroll
+            for (int i = 0; i < P; i += 2) {
+                const uint32_t o = order_of_pair(raw[i / 8][i % 8 / 2], size);
+                const uint32_t last = 0xFFFFu - static_cast<uint32_t>((i / 8 * L + sub) * 8 + i % 8);
+                key[i] = o << 16 | last;
+                key[i + 1] = (o & 0xFFFF0000u) | (last - 1);
+            }
+            Key most = key[0];
+#pragma unroll
+            for (int i = 1; i < P; ++i) most = max_key(most, key[i]);
+            m = logit_of_key<DT>(largest_key<L>(most));
+            const bool nan = size.x > kInfBits<DT> || size.y > kInfBits<DT>;
+            if (__builtin_amdgcn_ballot_w64(nan) != 0) bad = lanes_max<L>(nan ? 1.0f : 0.0f) > 0.0f;
+            bad |= !sigmoid && m == __builtin_inff();
+        } else {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                if (live) load8<DT>(x, (c * L + sub) * 8, n, EXACT ? -kTame : -__builtin_inff(), z + c * 8);
+                else
+                    for (int j = 0; j < 8; ++j) z[c * 8 + j] = 0.0f;
+            }
+            m = z[0];
+#pragma unroll
+            for (int i = 1; i < P; ++i) m = __builtin_fmaxf(m, z[i]);
+            m = __builtin_fmaxf(lanes_max<L>(m), -FLT_MAX);
         }
-        bool bad = false;
-        float m = z[0];
-#pragma unroll
-        for (int i = 1; i < P; ++i) m = __builtin_fmaxf(m, z[i]);
-        m = __builtin_fmaxf(lanes_max<L>(m), -FLT_MAX);
         // Are all logits of the wave's tokens of a size that needs no care?  (What is past a token's
         // experts is at the lower end then, closed, and adds nothing that shows to a sum.)
-        bool tame = false;
         if constexpr (EXACT) {
             float lo = z[0], hi = z[0];
 #pragma unroll
@@ -400,7 +466,7 @@ __global__ __launch_bounds__(kRouteThreads, (route_waves<DT, P, EXACT>())) void 
             for (int i = 0; i < P; i += 2) odd |= __builtin_isunordered(z[i], z[i + 1]);
             tame = __builtin_amdgcn_ballot_w64(odd) == 0;
         }
-        if (!tame) {
+        if constexpr (!PACKED) if (!tame) {
             if constexpr (EXACT) {
                 m = -FLT_MAX;
                 const int end = here(n);
@@ -418,7 +484,6 @@ __global__ __launch_bounds__(kRouteThreads, (route_waves<DT, P, EXACT>())) void 
         }
 
         // the scores, where the choice or a sum over the tokens wants all of them
-        Key key[P];
         double all = 0.0;
         bool some = live && some_open;  // is there an open expert?
         double part = 0.0;
@@ -490,36 +555,46 @@ __global__ __launch_bounds__(kRouteThreads, (route_waves<DT, P, EXACT>())) void 
                 for (int i = 0; i < P; ++i) total[i] = __builtin_fmaf(s[i], f, total[i]);
             }
         } else {
-            bool any = false;
-#pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const int e = (i / 8 * L + sub) * 8 + i % 8;
-                if constexpr (DT == kFP32) key[i] = key_of(static_cast<double>(z[i] + 0.0f), e);      // -0 is 0
-                else key[i] = key_of_logit<DT>(z[i], e);
-                const bool in = z[i] > -__builtin_inff();
-                any |= in;
-                if (!in) key[i] = no_key<Key>();
-            }
             if constexpr (DT == kFP32) {
+                bool any = false;
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    key[i] = key_of(static_cast<double>(z[i] + 0.0f), (i / 8 * L + sub) * 8 + i % 8);      // -0 is 0
+                    const bool in = z[i] > -__builtin_inff();
+                    any |= in;
+                    if (!in) key[i] = no_key<Key>();
+                }
                 if (sigmoid && m == __builtin_inff()) {         // its key would be a NaN's
 #pragma unroll
                     for (int i = 0; i < P; ++i)
                         if (z[i] == __builtin_inff()) key[i] = key_of(kMost, (i / 8 * L + sub) * 8 + i % 8);
                 }
+                some = live && !bad && lanes_max<L>(any ? 1.0f : 0.0f) > 0.0f;
+            } else {
+                some = live && !bad && m > -__builtin_inff();
+                m = __builtin_fmaxf(m, -FLT_MAX);
             }
-            some = live && !bad && lanes_max<L>(any ? 1.0f : 0.0f) > 0.0f;
             if (sums || !(sigmoid || a.renormalise)) {
                 float s[P], lane_sum = 0.0f;         // shares of a softmax, scores of a sigmoid
+                if constexpr (PACKED) {
 #pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    if (sigmoid) {
-                        const float u = exp2_hw(-__builtin_fabsf(z[i]) * static_cast<float>(kLog2E));
-                        s[i] = (z[i] >= 0.0f ? 1.0f : u) * __builtin_amdgcn_rcpf(1.0f + u);
-                    } else {
-                        s[i] = share_to_fast(z[i], m);
-                    }
-                    lane_sum += s[i];
+                    for (int c = 0; c < C; ++c) unpack<DT>(raw[c], reinterpret_cast<float(&)[8]>(s[c * 8]));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < P; ++i) s[i] = z[i];
                 }
+                if (sigmoid) {
+#pragma unroll
+                    for (int i = 0; i < P; ++i) {
+                        const float u = exp2_hw(-__builtin_fabsf(s[i]) * static_cast<float>(kLog2E));
+                        s[i] = (s[i] >= 0.0f ? 1.0f : u) * __builtin_amdgcn_rcpf(1.0f + u);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < P; ++i) s[i] = share_to_fast(s[i], m);
+                }
+#pragma unroll
+                for (int i = 0; i < P; ++i) lane_sum += s[i];
                 all = lanes_sum<L>(static_cast<double>(lane_sum));
                 part = all > 0.0 ? reciprocal(all) : 0.0;
                 if (sums) {
@@ -555,9 +630,9 @@ __global__ __launch_bounds__(kRouteThreads, (route_waves<DT, P, EXACT>())) void 
                     if (stride > 1) next = max_key(next, mine[(g * per + i) * stride + 1]);
                 }
                 if constexpr (EXACT) {
-                    if (a.group_best == 2 && is_open<Key, true>(best))
+                    if (a.group_best == 2 && is_open<DT, Key, true>(best))
                         best = __builtin_bit_cast(
-                            double, rounded(key_score(best) + (is_open<Key, true>(next) ? key_score(next) : 0.0)));
+                            double, rounded(key_score(best) + (is_open<DT, Key, true>(next) ? key_score(next) : 0.0)));
                 }
                 group_of[g] = best;
             }
@@ -628,7 +703,7 @@ __global__ __launch_bounds__(kRouteThreads, (route_waves<DT, P, EXACT>())) void 
 #pragma unroll
             for (int i = u * L; i < (u + 1) * L && i < K; ++i)
                 if (i == u * L + sub) own = list[i];
-            const bool there = !none && u * L + sub < a.top && is_open<Key, EXACT>(own);
+            const bool there = !none && u * L + sub < a.top && is_open<DT, Key, EXACT>(own);
             expert[u] = there ? key_expert(own) : -1;
             float ze = 0.0f;
             if (there) ze = widen<DT>(x[expert[u]]);
@@ -697,6 +772,7 @@ constexpr int kFinishThreads = 1024;
 constexpr int kFinishExperts = 16;
 constexpr int kFinishMost = MP_ROUTE_MAX_EXPERTS / kFinishExperts + 1;
 
+// 512 workgroups' sums of 256 experts: 6.8 us, of 128 workgroups' of 60: 4.6 us; bound by latency.
 __global__ __launch_bounds__(kFinishThreads) void k_route_finish(RouteArgs a, RouteSums w)
 {
     constexpr int SLICES = kFinishThreads / kFinishExperts, W = kFinishThreads / kWave, U = 4;
@@ -777,7 +853,9 @@ __global__ __launch_bounds__(kFinishThreads) void k_route_finish(RouteArgs a, Ro
 // the chosen experts' scores,
 //   softmax  dx_e = s_e (pull_e + ds_e - sum_j s_j (pull_j + ds_j) + 2 F z lse)
 //   sigmoid  dx_e = s_e (1 - s_e) ((pull_e - sum_j p_j pull_j) / sum s + ds_e),    p = s / sum s.
-// L lanes per token and P experts a lane, as in the choice.
+// L lanes per token and P experts a lane, as in the choice.  fp32 but for the sums over a token: nothing here is
+// compared.  65536 x 256 bf16 by sigmoid: 25 us, 2.7 TB/s read and written; the vector units are at
+// work 70 of 100 cycles, two of 33 instructions an expert being an exponential and a reciprocal.
 template <int DT, int L, int P, bool SIGMOID>
 __global__ __launch_bounds__(kRouteThreads) void k_route_grad(RouteGradArgs a)
 {
@@ -971,6 +1049,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_grad(RouteGradArgs a)
 }
 
 // out = bias + speed sign(mean load - load), one workgroup a layer; a skipped step leaves the bias.
+// 256 experts: 4.5 us, a launch and two dependent reads.
 __global__ __launch_bounds__(kRouteThreads) void k_route_bias(RouteBiasArgs a)
 {
     __shared__ int64_t part[kRouteWaves];
@@ -1009,13 +1088,12 @@ int64_t route_grid(int64_t rows, int lanes, int64_t most)
 template <int DT, int L, int P, int K, bool EXACT>
 void route_shape(const RouteArgs& a, RouteSums& w, hipStream_t s)
 {
-    // with sums, as many workgroups as are resident at once: each leaves sums of its own
-    constexpr int64_t resident = 256 * route_waves<DT, P, EXACT>();
-    int64_t most = 1 << 16;
-    if (a.load != nullptr) {
-        most = (MP_ROUTE_WORKSPACE_BYTES - kFinishMost * 8 - 16) / (12 * (int64_t(a.x.vocab) + 1));
-        if (most > resident) most = resident;
-    }
+    // As many workgroups as are resident at once: a start costs a wave as much as a tenth of a token's work
+    // (131072 x 128 bf16 18.7 us, 20.3 with a workgroup for every 32 tokens; 65536 x 256 by a bias
+    // 52.9 and 60.1), and with sums each leaves its own.
+    int64_t most = 256 * route_waves<DT, P, EXACT>();
+    if (a.load != nullptr)
+        most = std::min<int64_t>(most, (MP_ROUTE_WORKSPACE_BYTES - kFinishMost * 8 - 16) / (12 * (int64_t(a.x.vocab) + 1)));
     const int64_t grid = route_grid(a.x.rows, L, most);
     if (a.load != nullptr) {
         w.groups = static_cast<int>(grid);
