@@ -787,15 +787,15 @@ typedef struct {
     void* workspace;
 } mp_routed;
 
-/* c and the groups' sums are formed in binary64 and compared after rounding to 42 bits
- * (without a bias, and unless groups of group_best 2 are summed, the order is the
- * logits', also where their scores round alike).
- * An expert whose logit is -inf, or whose bias is -inf or NaN, is closed (any other
- * bias beyond 1e38 in size counts as that); a logit of -inf has s = 0.  A sigmoid below 2^-1000 is 0, and p = 0 where all of a token's
- * are.  A token with fewer open experts than `top` has ids -1 and weights 0 at its
- * end; one with none is not among the tokens routed.  A token without a distribution (a NaN; with softmax
- * also +inf, or nothing but -inf) has ids -1 and weights NaN and is in no sum.
- * bias: experts fp32, or NULL: 0. */
+/* c and the groups' sums are formed in binary64 and compared after rounding to 42
+ * bits (without a bias, and unless groups of group_best 2 are summed, the order is
+ * the logits', also where their scores round alike).  An expert whose logit is -inf,
+ * or whose bias is -inf or NaN, is closed (any other bias beyond 1e38 in size counts
+ * as that); a logit of -inf has s = 0.  A sigmoid below 2^-1000 is 0, and p = 0 where
+ * all of a token's are.  A token with fewer open experts than `top` has ids -1 and
+ * weights 0 at its end; one with none is not among the tokens routed.  A token without
+ * a distribution (a NaN; with softmax also +inf, or nothing but -inf) has ids -1 and
+ * weights NaN and is in no sum. */
 mp_status mp_route(const mp_logits* x, const float* bias, const uint8_t* mask,
                    const mp_route_cfg* cfg, const mp_routed* out, mp_stream stream);
 

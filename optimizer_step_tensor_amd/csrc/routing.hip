@@ -354,11 +354,11 @@ __host__ __device__ __forceinline__ int group_keys(int n, int groups, int all)
 }
 
 // L lanes per token, P experts a lane: expert (c L + lane) 8 + j is the lane's P's c 8 + j.
-// Bound by the vector units.  131072 x 128 bf16, 8 of 128 by logits: 23.5 us, 93 of 100 cycles of them, 43
-// instructions an expert and lane with the sorting, against 7 us for reads and writes.  65536 x 256 bf16,
-// 8 of 256 by a bias in 4 of 8 groups, with sums: 58 us, 82 instructions of which the binary64
-// score is 32; two waves a SIMD, all that 16 experts' keys leave room for, keep the units at work
-// two thirds of the time.  7 x 64: 3.2 us, a launch.
+// Bound by the vector units.  131072 x 128 bf16, 8 of 128 by logits: 19 us against 7 us for reads and
+// writes; of some 470 instructions for 16 experts a lane 206 sort.  65536 x 256 bf16, 8 of 256 by a bias in 4
+// of 8 groups, with sums: 57 us, 82 instructions an expert, of which the binary64 score is 32; two
+// waves a SIMD, all that 16 experts' keys leave room for, keep the units at work two thirds of the
+// time.  (Eight experts a lane and four waves: 64 us without sums, 52 with 16.)  7 x 64: 3.2 us, a launch.
 template <int DT, int L, int P, int K, bool EXACT>
 __global__ __launch_bounds__(kRouteThreads, (route_waves<DT, P, EXACT>())) void k_route(RouteArgs a, RouteSums w, int space_bytes)
 {
