@@ -273,6 +273,23 @@ __device__ __forceinline__ void join_lanes(Key (&k)[K])
     }
 }
 
+// The sum over the lanes that are a multiple of L apart.
+template <int L>
+__device__ __forceinline__ double tokens_sum(double v)
+{
+    if constexpr (L == kWave) return v;
+    else if constexpr (L == 8) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, v);
+        constexpr int rotate8 = 0x128;              // of 16 lanes
+        const int lo = __builtin_amdgcn_mov_dpp(static_cast<int>(u), rotate8, 0xF, 0xF, true);
+        const int hi = __builtin_amdgcn_mov_dpp(static_cast<int>(u >> 32), rotate8, 0xF, 0xF, true);
+        return tokens_sum<16>(v + __builtin_bit_cast(double, uint64_t(static_cast<uint32_t>(hi)) << 32 |
+                                                                 static_cast<uint32_t>(lo)));
+    } else {
+        return tokens_sum<2 * L>(v + partner<L>(v));
+    }
+}
+
 constexpr int kRouteThreads = 256;
 constexpr int kRouteWaves = kRouteThreads / kWave;
 constexpr double kTiny = 1e-20;
@@ -735,19 +752,14 @@ __global__ __launch_bounds__(kRouteThreads, (route_waves<DT, P, EXACT>())) void 
     // a wave's tokens had the same lanes: their sums, then the waves', in this order
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-        double v = static_cast<double>(total[i]);
-#pragma unroll
-        for (int o = L; o < kWave; o *= 2) v += __shfl_xor(v, o);
+        const double v = tokens_sum<L>(static_cast<double>(total[i]));
         if (slot == 0) reinterpret_cast<double*>(own_space)[(i / 8 * L + sub) * 8 + i % 8] = v;
     }
-#pragma unroll
-    for (int o = 1; o < kWave; o *= 2) {
-        squares += __shfl_xor(squares, o);
-        tokens += __shfl_xor(tokens, o);
-    }
+    squares = lanes_sum<kWave>(squares);
+    const double all_tokens = lanes_sum<kWave>(static_cast<double>(tokens));
     if (lane == 0) {
         square[wave] = squares;
-        routed[wave] = tokens;
+        routed[wave] = static_cast<int32_t>(all_tokens);
     }
     __syncthreads();
     double* share = w.share + int64_t(blockIdx.x) * (n + 1);
