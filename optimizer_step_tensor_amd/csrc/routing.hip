@@ -356,11 +356,15 @@ __device__ __forceinline__ void wave_fence()
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 }
 
-// Waves a SIMD that k_route's registers leave room for.
-template <int DT, int P, bool EXACT>
+// Waves a SIMD that k_route's registers leave room for, without scratch.  Without sums that is one or two more
+// (65536 x 256 by a bias 43 us, 52 in the form with sums; 131072 x 128 by logits 17.1 and 18.5; 131072 x
+// 64 12.4 and 14.1).
+template <int DT, int L, int P, bool EXACT, bool SUMS>
 constexpr int route_waves()
 {
-    return EXACT && P == 16 ? 2 : EXACT || DT == kFP32 ? 3 : 4;
+    if (SUMS) return EXACT && P == 16 ? 2 : EXACT || DT == kFP32 ? 3 : 4;
+    if (EXACT) return P == 8 ? 4 : DT == kFP16 && L == 8 ? 2 : 3;
+    return DT == kFP32 ? (P == 8 ? 5 : 3) : P == 8 ? 7 : 5;
 }
 
 // Places for keys that the groups of a token are formed from: two for each chunk, or all experts where
@@ -371,13 +375,14 @@ __host__ __device__ __forceinline__ int group_keys(int n, int groups, int all)
 }
 
 // L lanes per token, P experts a lane: expert (c L + lane) 8 + j is the lane's P's c 8 + j.
-// Bound by the vector units.  131072 x 128 bf16, 8 of 128 by logits: 19 us against 7 us for reads and
-// writes; of some 470 instructions for 16 experts a lane 206 sort.  65536 x 256 bf16, 8 of 256 by a bias in 4
-// of 8 groups, with sums: 57 us, 82 instructions an expert, of which the binary64 score is 32; two
+// Bound by the vector units.  131072 x 128 bf16, 8 of 128 by logits: 17 us against 7 us for reads and
+// writes; of some 460 instructions for 16 experts a lane 206 sort.  65536 x 256 bf16, 8 of 256 by a bias in 4
+// of 8 groups, with sums: 58 us, 82 instructions an expert, of which the binary64 score is 32; two
 // waves a SIMD, all that 16 experts' keys leave room for, keep the units at work two thirds of the
 // time.  (Eight experts a lane and four waves: 64 us without sums, 52 with 16.)  7 x 64: 3.2 us, a launch.
-template <int DT, int L, int P, int K, bool EXACT>
-__global__ __launch_bounds__(kRouteThreads, (route_waves<DT, P, EXACT>())) void k_route(RouteArgs a, RouteSums w, int space_bytes)
+template <int DT, int L, int P, int K, bool EXACT, bool SUMS>
+__global__ __launch_bounds__(kRouteThreads, (route_waves<DT, L, P, EXACT, SUMS>()))
+void k_route(RouteArgs a, RouteSums w, int space_bytes)
 {
     using T = typename Fmt<DT>::T;
     using Key = std::conditional_t<EXACT || DT == kFP32, double, uint32_t>;
@@ -393,7 +398,7 @@ __global__ __launch_bounds__(kRouteThreads, (route_waves<DT, P, EXACT>())) void 
     const int sub = lane % L, slot = lane / L;
     const int n = a.x.vocab;
     const int width = n / a.groups;
-    const bool sums = w.share != nullptr, sigmoid = a.sigmoid != 0;
+    const bool sigmoid = a.sigmoid != 0;
     // this token's keys, the groups' and whether these are open
     const int keys = group_keys(n, a.groups, N);
     char* const own_space = space + wave * space_bytes;
@@ -401,14 +406,14 @@ __global__ __launch_bounds__(kRouteThreads, (route_waves<DT, P, EXACT>())) void 
     Key* const group_of = mine + keys;
     uint8_t* const open_of = reinterpret_cast<uint8_t*>(reinterpret_cast<Key*>(own_space) + R * (keys + a.groups)) +
                              slot * a.groups;
-    // A lane's sums are fp32, of 2^22 tokens over at least 1364 waves (binary64 ones would take sixteen registers
-    // more than there are for three waves a SIMD): below 3100 additions, 2^-12.4 relative if all of them
-    // were off the same way.  The lanes' are joined in binary64.
+    // A lane's sums are fp32 (binary64 ones would take sixteen registers more than there are), of 2^22 tokens
+    // over at least 1364 waves: below 3100 additions, 2^-12.4 relative if all were off the same way.
+    // The lanes' are joined in binary64.
     float total[P] = {};
     double squares = 0.0;
     int tokens = 0;
     bool some_open = true;              // some expert that the bias leaves open
-    if (sums) {
+    if constexpr (SUMS) {
         if (blockIdx.x == 0 && threadIdx.x == 0) *w.done = 0;
         for (int e = threadIdx.x; e < N; e += kRouteThreads) count[e] = 0;
         __syncthreads();
@@ -566,7 +571,7 @@ __global__ __launch_bounds__(kRouteThreads, (route_waves<DT, P, EXACT>())) void 
                 if (bad) part = 0.0;
                 some = live && !bad && lanes_max<L>(any ? 1.0f : 0.0f) > 0.0f;
             }
-            if (sums) {
+            if (SUMS) {
                 const float f = !some ? 0.0f : sigmoid ? static_cast<float>(part) : 1.0f;
 #pragma unroll
                 for (int i = 0; i < P; ++i) total[i] = __builtin_fmaf(s[i], f, total[i]);
@@ -591,7 +596,7 @@ __global__ __launch_bounds__(kRouteThreads, (route_waves<DT, P, EXACT>())) void 
                 some = live && !bad && m > -__builtin_inff();
                 m = __builtin_fmaxf(m, -FLT_MAX);
             }
-            if (sums || !(sigmoid || a.renormalise)) {
+            if (SUMS || !(sigmoid || a.renormalise)) {
                 float s[P], lane_sum = 0.0f;         // shares of a softmax, scores of a sigmoid
                 if constexpr (PACKED) {
 #pragma unroll
@@ -614,7 +619,7 @@ __global__ __launch_bounds__(kRouteThreads, (route_waves<DT, P, EXACT>())) void 
                 for (int i = 0; i < P; ++i) lane_sum += s[i];
                 all = lanes_sum<L>(static_cast<double>(lane_sum));
                 part = all > 0.0 ? reciprocal(all) : 0.0;
-                if (sums) {
+                if (SUMS) {
                     const float f = some ? static_cast<float>(part) : 0.0f;
 #pragma unroll
                     for (int i = 0; i < P; ++i) total[i] = __builtin_fmaf(some ? s[i] : 0.0f, f, total[i]);
@@ -738,9 +743,9 @@ __global__ __launch_bounds__(kRouteThreads, (route_waves<DT, P, EXACT>())) void 
             if (i >= a.top || row >= a.x.rows) continue;
             a.weights[int64_t(row) * a.top + i] = nan ? __builtin_nanf("") : static_cast<float>(weight[u] * unit);
             a.ids[int64_t(row) * a.top + i] = expert[u];
-            if (sums && expert[u] >= 0) atomicAdd(&count[expert[u]], 1);
+            if (SUMS && expert[u] >= 0) atomicAdd(&count[expert[u]], 1);
         }
-        if (sums && some && sub == 0) {
+        if (SUMS && some && sub == 0) {
             ++tokens;
             if (!sigmoid) {
                 const double lse = static_cast<double>(m) + log_sum(all);
@@ -748,7 +753,7 @@ __global__ __launch_bounds__(kRouteThreads, (route_waves<DT, P, EXACT>())) void 
             }
         }
     }
-    if (!sums) return;
+    if (!SUMS) return;
     // a wave's tokens had the same lanes: their sums, then the waves', in this order
 #pragma unroll
     for (int i = 0; i < P; ++i) {
@@ -1103,8 +1108,9 @@ void route_shape(const RouteArgs& a, RouteSums& w, hipStream_t s)
     // As many workgroups as are resident at once: a start costs a wave as much as a tenth of a token's work
     // (131072 x 128 bf16 18.7 us, 20.3 with a workgroup for every 32 tokens; 65536 x 256 by a bias
     // 52.9 and 60.1), and with sums each leaves its own.
-    int64_t most = 256 * route_waves<DT, P, EXACT>();
-    if (a.load != nullptr)
+    const bool sums = a.load != nullptr;
+    int64_t most = 256 * (sums ? route_waves<DT, L, P, EXACT, true>() : route_waves<DT, L, P, EXACT, false>());
+    if (sums)
         most = std::min<int64_t>(most, (MP_ROUTE_WORKSPACE_BYTES - kFinishMost * 8 - 16) / (12 * (int64_t(a.x.vocab) + 1)));
     const int64_t grid = route_grid(a.x.rows, L, most);
     if (a.load != nullptr) {
@@ -1119,10 +1125,11 @@ void route_shape(const RouteArgs& a, RouteSums& w, hipStream_t s)
     constexpr int key_bytes = EXACT || DT == kFP32 ? 8 : 4;
     int space = 0;
     if (a.groups > 1) space = R * ((group_keys(a.x.vocab, a.groups, N) + a.groups) * key_bytes + a.groups);
-    if (a.load != nullptr && space < N * 8) space = N * 8;
+    if (sums && space < N * 8) space = N * 8;
     space = (space + 15) / 16 * 16;
-    k_route<DT, L, P, K, EXACT>
-        <<<static_cast<unsigned>(grid), kRouteThreads, static_cast<unsigned>(space * kRouteWaves), s>>>(a, w, space);
+    const unsigned blocks = static_cast<unsigned>(grid), bytes = static_cast<unsigned>(space * kRouteWaves);
+    if (sums) k_route<DT, L, P, K, EXACT, true><<<blocks, kRouteThreads, bytes, s>>>(a, w, space);
+    else k_route<DT, L, P, K, EXACT, false><<<blocks, kRouteThreads, bytes, s>>>(a, w, space);
 }
 
 template <int DT, int K, bool EXACT>
