@@ -112,6 +112,35 @@ def test_tokens(mp, rows):
     check_route(mp, x, "bf16", 2, True, f32(rng.normal(0, 0.1, 64)), None, 8, 3, 2)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n,groups,top,tokens", [(60, 1, 4, 80), (64, 4, 9, 80), (128, 8, 8, 60), (256, 8, 8, 30),
+                                                 (512, 1, 12, 20), (1000, 1, 6, 10)])
+def test_more_tokens_than_are_at_work_at_once(mp, kind, n, groups, top, tokens):
+    """A wave's second and later tokens, in every form: `tokens` times 1009 that are alike."""
+    import torch
+    x = router(gen(52, n), 1009, n, kind)
+    bias = f32(0.05 * gen(53, n).normal(0, 1, n))
+    rows = 1009 * tokens
+    b = Buf(rows, n, kind, 8, 0, np.resize(x, (rows, n)))
+    mask = np.arange(1009) % 7 != 3
+    m = torch.as_tensor(np.resize(mask, rows), device="cuda")
+    for given, sigmoid, keep, best in ((None, False, max(1, groups // 2), 1), (bias, True, max(1, groups // 2), 2)):
+        want = ref.route(x, given, mask, sigmoid, top, groups, keep, best, True, 1.0)
+        cfg = mp.route_cfg(top, int(sigmoid), groups, keep, best, True, 1.0)
+        for train in (False, True):
+            o = Out(mp, rows, top, n if train else None)
+            mp.mp_route(mp.logits(b.t), None if given is None else dev(given), m, cfg, o.struct)
+            assert np.array_equal(o.ids.cpu().numpy(), np.resize(want["ids"], (rows, top)))
+            check("weights", o.weights, np.resize(want["weights"], (rows, top)),
+                  np.resize(want["tol_weights"], (rows, top)))
+            if train:
+                assert np.array_equal(o.load.cpu().numpy(), want["load"] * tokens)
+                # a lane adds up at most ten tokens, of a thousand and more at once; they count in fp32
+                more = 10 * 2.0 ** -24 * want["share"]
+                check("share", o.share, want["share"], want["tol_share"] + more)
+            assert o.untouched() and b.untouched()
+
+
 @pytest.mark.parametrize("sigmoid", [False, True])
 @pytest.mark.parametrize("n", [8, 60, 256, 600])
 def test_equal_scores_take_the_lowest_number(mp, n, sigmoid):
