@@ -1,6 +1,7 @@
 """Build libmpstep.so (the HIP kernels and the C ABI of include/mpstep.h) for gfx950."""
 import os
 import subprocess
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -30,10 +31,17 @@ SANITIZE_HOST = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize
 
 
 def build(out=LIB, extra=(), sanitize=False):
-    """Compile the library (always recompiles); returns its path."""
+    """Compile the library (always recompiles), a process a source; returns its path."""
     tmp = out + ".tmp"
-    cmd = [HIPCC, *FLAGS, *(SANITIZE_HOST if sanitize else ()), *extra, "-o", tmp, *SOURCES]
-    subprocess.run(cmd, check=True)
+    flags = [*FLAGS, *(SANITIZE_HOST if sanitize else ()), *extra]
+    with tempfile.TemporaryDirectory() as d:
+        objects = [os.path.join(d, os.path.basename(s) + ".o") for s in SOURCES]
+        cmds = [[HIPCC, *[f for f in flags if f != "-shared"], "-c", "-o", o, s]
+                for o, s in zip(objects, SOURCES)]
+        running = [subprocess.Popen(c) for c in cmds]
+        for p, c in [(p, c) for p, c in zip(running, cmds) if p.wait() != 0]:
+            raise subprocess.CalledProcessError(p.returncode, c)
+        subprocess.run([HIPCC, *flags, "-o", tmp, *objects], check=True)
     os.replace(tmp, out)
     return out
 
