@@ -798,6 +798,9 @@ def mp_route_grad(x, mask, cfg, ids, dweights, load, balance_coef, z_coef, grad,
     """ids and dweights: int64 and float32 [tokens, top] (dweights may be None); load: int64
     [experts + 1], or None without auxiliary losses; grad: logits_grad(...), written."""
     n, d = _place(x)
+    for t, name in ((ids, "ids"), (dweights, "dweights")):
+        if isinstance(t, torch.Tensor) and t.dim() > 1 and t.shape[-1] != cfg.top:
+            raise ValueError("%s must have %d columns" % (name, cfg.top))
     _check(lib().mp_route_grad(ctypes.byref(x), _mask(mask, n, d), ctypes.byref(cfg),
                                _array(ids, _I64, n * cfg.top, "ids", d),
                                _array(dweights, _F32, n * cfg.top, "dweights", d),

@@ -382,6 +382,15 @@ def test_binding_refuses_what_does_not_fit(mp):
         mp.mp_route(lx, None, None, mp.route_cfg(2), Out(mp, 4, 2).struct)
 
 
+def test_binding_refuses_lists_of_another_length(mp):
+    import torch
+    x, dx = torch.zeros(4, 8, device="cuda"), torch.zeros(4, 8, device="cuda")
+    ids, dw = torch.zeros(4, 3, dtype=torch.int64, device="cuda"), torch.zeros(4, 3, device="cuda")
+    for i, d, name in ((ids, dw[:, :2].contiguous(), "ids"), (ids[:, :2].contiguous(), dw, "dweights")):
+        with pytest.raises(ValueError, match=name + " must have 2 columns"):
+            mp.mp_route_grad(mp.logits(x), None, mp.route_cfg(2), i, d, None, 0.0, 0.0, mp.logits_grad(dx))
+
+
 # --- together, as a training program uses them ------------------------------------------------------
 
 @pytest.mark.parametrize("sigmoid", [False, True])
