@@ -304,9 +304,13 @@ struct RouteSums {
     int groups;         // workgroups
 };
 
-// Logits up to this size, and tokens whose largest is not below a quarter of it on that side, have
-// exponentials and sums in binary64's middle range.
+// Logits up to this size, and tokens whose largest is not below a quarter of it on that side (kLow for a sigmoid's
+// sums: fp32 holds the scores and their sum's reciprocal then), have exponentials and sums in binary64's middle range.
 constexpr float kTame = 340.0f;
+
+// A token whose logits are all below this: its sigmoids are exp(z) to fp32's last bit, and from here on leave
+// fp32's range, or its normal numbers, sooner than their shares do, which are a softmax's.
+constexpr float kLow = -32.0f;
 
 // n, for comparisons that are formed where they are used and not, sixteen lane masks of them, kept over
 // a loop.
@@ -483,7 +487,7 @@ void k_route(RouteArgs a, RouteSums w, int space_bytes)
                 lo = __builtin_fminf(lo, z[i]);
                 hi = __builtin_fmaxf(hi, z[i]);
             }
-            bool odd = !(lo >= -kTame && hi <= kTame && m >= -kTame / 4);
+            bool odd = !(lo >= -kTame && hi <= kTame && m >= (SUMS && sigmoid ? kLow : -kTame / 4));
 #pragma unroll
             for (int i = 0; i < P; i += 2) odd |= __builtin_isunordered(z[i], z[i + 1]);
             tame = __builtin_amdgcn_ballot_w64(odd) == 0;
@@ -510,7 +514,7 @@ void k_route(RouteArgs a, RouteSums w, int space_bytes)
         bool some = live && some_open;  // is there an open expert?
         double part = 0.0;
         if constexpr (EXACT) {
-            float s[P];                  // shares of a softmax, scores of a sigmoid: for the sums
+            float s[P];                  // for the sums: shares, but scores of a tame sigmoid
             // four experts' arithmetic at a time: all sixteen at once would take all registers
             auto four = [](int i) {
                 if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);
@@ -561,8 +565,8 @@ void k_route(RouteArgs a, RouteSums w, int space_bytes)
                 part = all > 0.0 ? reciprocal(all) : 0.0;
 #pragma unroll
                 for (int i = 0; i < P; ++i) {
-                    const double c = sigmoid ? key[i] : key[i] * part;
-                    s[i] = bad ? 0.0f : static_cast<float>(c);         // NaN times 0 would be in the sums
+                    const double p = key[i] * part, c = sigmoid ? key[i] : p;
+                    s[i] = bad ? 0.0f : static_cast<float>(p);         // NaN times 0 would be in the sums
                     const float bias = z[i] > -__builtin_inff() ? bias_of[number(i)] : kClosed;
                     any |= bias > kClosed;
                     key[i] = key_of((bias > kClosed ? c : 0.0) + static_cast<double>(bias), number(i));
@@ -572,7 +576,7 @@ void k_route(RouteArgs a, RouteSums w, int space_bytes)
                 some = live && !bad && lanes_max<L>(any ? 1.0f : 0.0f) > 0.0f;
             }
             if (SUMS) {
-                const float f = !some ? 0.0f : sigmoid ? static_cast<float>(part) : 1.0f;
+                const float f = !some ? 0.0f : sigmoid && tame ? static_cast<float>(part) : 1.0f;
 #pragma unroll
                 for (int i = 0; i < P; ++i) total[i] = __builtin_fmaf(s[i], f, total[i]);
             }
