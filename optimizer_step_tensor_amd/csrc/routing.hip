@@ -98,6 +98,17 @@ __device__ __forceinline__ float share_to_fast(float z, float m)
     return exp2_hw(__builtin_fmaf(t, lo, t * hi));
 }
 
+// A token whose logits are all below this: its sigmoids are exp(z) to fp32's last bit, and from here on leave
+// fp32's range, or its normal numbers, sooner than their shares do, which are a softmax's.
+constexpr float kLow = -32.0f;
+
+// A sigmoid of a token whose largest logit m is below kLow, relative to exp(m); 0 below 2^-1000 as in score_of.
+constexpr float kNothing = -693.14718f;                  // -1000 ln 2
+__device__ __forceinline__ float low_share(float z, float m)
+{
+    return z < kNothing ? 0.0f : share_to_fast(z, m);
+}
+
 constexpr int kIdBits = 10;                              // MP_ROUTE_MAX_EXPERTS is 2^10
 constexpr uint64_t kIdMask = (1 << kIdBits) - 1;
 
@@ -307,10 +318,6 @@ struct RouteSums {
 // Logits up to this size, and tokens whose largest is not below a quarter of it on that side (kLow for a sigmoid's
 // sums: fp32 holds the scores and their sum's reciprocal then), have exponentials and sums in binary64's middle range.
 constexpr float kTame = 340.0f;
-
-// A token whose logits are all below this: its sigmoids are exp(z) to fp32's last bit, and from here on leave
-// fp32's range, or its normal numbers, sooner than their shares do, which are a softmax's.
-constexpr float kLow = -32.0f;
 
 // n, for comparisons that are formed where they are used and not, sixteen lane masks of them, kept over
 // a loop.
@@ -609,12 +616,17 @@ void k_route(RouteArgs a, RouteSums w, int space_bytes)
 #pragma unroll
                     for (int i = 0; i < P; ++i) s[i] = z[i];
                 }
-                if (sigmoid) {
+                auto score = [](float v) {
+                    const float u = exp2_hw(-__builtin_fabsf(v) * static_cast<float>(kLog2E));
+                    return (v >= 0.0f ? 1.0f : u) * __builtin_amdgcn_rcpf(1.0f + u);
+                };
+                const bool low = sigmoid && m < kLow;
+                if (__builtin_amdgcn_ballot_w64(low) != 0) {
 #pragma unroll
-                    for (int i = 0; i < P; ++i) {
-                        const float u = exp2_hw(-__builtin_fabsf(s[i]) * static_cast<float>(kLog2E));
-                        s[i] = (s[i] >= 0.0f ? 1.0f : u) * __builtin_amdgcn_rcpf(1.0f + u);
-                    }
+                    for (int i = 0; i < P; ++i) s[i] = low ? low_share(s[i], m) : score(s[i]);
+                } else if (sigmoid) {
+#pragma unroll
+                    for (int i = 0; i < P; ++i) s[i] = score(s[i]);
                 } else {
 #pragma unroll
                     for (int i = 0; i < P; ++i) s[i] = share_to_fast(s[i], m);

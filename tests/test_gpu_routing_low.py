@@ -39,3 +39,25 @@ def test_shares_of_low_tokens_by_a_bias(mp, kind, n):  # noqa: F811
     check_shares(mp, kind, n, f32(0.05 * gen(59, n).normal(0, 1, n)))
     if n % 4 == 0:                      # sums of two scores are binary64 too
         check_shares(mp, kind, n, None, groups=4, top_groups=2, best=2)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n", [3, 60, 100, 256, 400, 1000])
+def test_shares_of_low_tokens_by_logits(mp, kind, n):  # noqa: F811
+    check_shares(mp, kind, n, None)
+    if n % 4 == 0:
+        check_shares(mp, kind, n, None, groups=4, top_groups=2, best=1)
+
+
+@pytest.mark.parametrize("biased", [True, False])
+def test_a_low_token_does_not_change_others(mp, biased):  # noqa: F811
+    """The choice and the weights of the tokens that share a wave with low ones."""
+    rng = gen(62)
+    x = low(rng, 0.0, 64, 60, "bf16")
+    bias = f32(0.05 * rng.normal(0, 1, 60)) if biased else None
+    a, _, _ = check_route(mp, x, "bf16", 6, True, bias)
+    y = x.copy()
+    y[::3] = low(rng, -100.0, 22, 60, "bf16")
+    b, _, _ = check_route(mp, y, "bf16", 6, True, bias)
+    keep = np.arange(64) % 3 != 0
+    assert np.array_equal(a.ids.cpu().numpy()[keep], b.ids.cpu().numpy()[keep])
