@@ -809,8 +809,9 @@ mp_status mp_route(const mp_logits* x, const float* bias, const uint8_t* mask,
  * a token without one has a gradient of 0, or NaN without a distribution.  An id
  * >= experts makes the token's gradient NaN, and no memory is read there; an id that
  * comes twice counts twice.  z_coef must be 0 with sigmoid scores.  Formed in
- * fp32 (a sigmoid below 2^-126 is 0), with sums over a token in binary64, and
- * rounded once. */
+ * fp32, with sums over a token in binary64, and rounded once.  A sigmoid below 2^-126
+ * is 0 (of a token whose logits are all below -32 the balance loss takes shares to
+ * 2^-1000, as mp_route). */
 mp_status mp_route_grad(const mp_logits* x, const uint8_t* mask, const mp_route_cfg* cfg,
                         const int64_t* ids, const float* dweights, const int64_t* load,
                         float balance_coef, float z_coef, const mp_logits_grad* grad,

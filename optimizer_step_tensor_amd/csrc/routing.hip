@@ -886,11 +886,13 @@ __global__ __launch_bounds__(kFinishThreads) void k_route_finish(RouteArgs a, Ro
 // the chosen experts' scores,
 //   softmax  dx_e = s_e (pull_e + ds_e - sum_j s_j (pull_j + ds_j) + 2 F z lse)
 //   sigmoid  dx_e = s_e (1 - s_e) ((pull_e - sum_j p_j pull_j) / sum s + ds_e),    p = s / sum s.
+// (of a token whose logits are all below kLow s and sum s are relative to its largest one's, and ds is scaled instead).
 // L lanes per token and P experts a lane, as in the choice.  fp32 but for the sums over a token: nothing here is
 // compared.  65536 x 256 bf16 by sigmoid: 25 us, 2.7 TB/s read and written; the vector units are at
 // work 70 of 100 cycles, two of 33 instructions an expert being an exponential and a reciprocal.
+// At most 128 registers, for four waves a SIMD (one kernel would take 130).
 template <int DT, int L, int P, bool SIGMOID>
-__global__ __launch_bounds__(kRouteThreads) void k_route_grad(RouteGradArgs a)
+__global__ __launch_bounds__(kRouteThreads, 4) void k_route_grad(RouteGradArgs a)
 {
     using T = typename Fmt<DT>::T;
     constexpr int E = Fmt<DT>::E;
@@ -964,12 +966,23 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_grad(RouteGradArgs a)
             u = t * r * r;
             return v >= 0.0f ? r : t * r;
         };
+        const bool low = SIGMOID && live && m < kLow;
+        const bool some_low = __builtin_amdgcn_ballot_w64(low) != 0;
+        if constexpr (!SIGMOID) {
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            if constexpr (SIGMOID) s[i] = score(z[i], slope[i]);
-            else s[i] = share_to_fast(z[i], m);
-            lane_sum += s[i];
+            for (int i = 0; i < P; ++i) s[i] = share_to_fast(z[i], m);
+        } else if (some_low) {
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                s[i] = score(z[i], slope[i]);
+                if (low) s[i] = slope[i] = low_share(z[i], m);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < P; ++i) s[i] = score(z[i], slope[i]);
         }
+#pragma unroll
+        for (int i = 0; i < P; ++i) lane_sum += s[i];
         const double all = lanes_sum<L>(static_cast<double>(lane_sum));
         const bool nan = live && (bad || (!SIGMOID && !(all > 0.0)));
         const bool on = live && any && !nan;
@@ -997,6 +1010,11 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_grad(RouteGradArgs a)
         } else {
 #pragma unroll
             for (int u = 0; u < U; ++u) ds[u] = static_cast<double>(dw[u]);
+        }
+        if (some_low) {
+            const double down = low ? exp_of(static_cast<double>(m)) : 1.0;      // the scores are relative to it
+#pragma unroll
+            for (int u = 0; u < U; ++u) ds[u] *= down;
         }
         // each writes its own number where its ds will be: an expert that is there twice shows
         wave_fence();
@@ -1063,7 +1081,8 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_grad(RouteGradArgs a)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int i = c * 8 + j;
-                if constexpr (SIGMOID) f[j] = slope[i] * ((pull[i] - base) * part + to[i]);
+                // (slope * part is below 1; part alone times a pull might leave fp32's range)
+                if constexpr (SIGMOID) f[j] = __builtin_fmaf(slope[i] * part, pull[i] - base, slope[i] * to[i]);
                 else f[j] = s[i] * (to[i] + base);
                 if (!on) f[j] = off;
             }

@@ -3,7 +3,8 @@ but their shares p = s / sum s do not -- the shares' means, the balance loss and
 import numpy as np
 import pytest
 
-from test_gpu_losses import KINDS, f32, gen, ttype
+import route_reference as ref
+from test_gpu_losses import KINDS, Buf, check, dev, f32, gen, ttype
 from test_gpu_routing import check_route, mp  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -61,3 +62,49 @@ def test_a_low_token_does_not_change_others(mp, biased):  # noqa: F811
     b, _, _ = check_route(mp, y, "bf16", 6, True, bias)
     keep = np.arange(64) % 3 != 0
     assert np.array_equal(a.ids.cpu().numpy()[keep], b.ids.cpu().numpy()[keep])
+
+
+# --- the gradient ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n", [3, 60, 100, 256, 400, 1000])
+@pytest.mark.parametrize("renormalise", [True, False])
+def test_gradient_of_low_tokens(mp, kind, n, renormalise):  # noqa: F811
+    """With factors up to an ordinary loss scale: a product of 1 / sum s and the pull of a balance loss would leave
+    fp32's range where the gradient is an ordinary number."""
+    rng = gen(61, n)
+    top, balance = min(n, 4), float(np.float32(0.01))
+    for level in LEVELS[:-2]:
+        for scale, with_dw in ((65536.0, False), (65536.0, True), (2.0 ** -10, False), (1.0, True)):
+            x = low(rng, level, 9, n, kind)
+            r = ref.route(x, None, None, True, top, renormalise=renormalise)
+            dw = f32(rng.normal(0, 1, (9, top)) * scale) if with_dw else None
+            b, bd = Buf(9, n, kind, 0, 0, x), Buf(9, n, kind, 3, 1)
+            g = mp.logits_grad(bd.t, 1.0, dev_scale=dev(np.float32([scale])))
+            mp.mp_route_grad(mp.logits(b.t), None, mp.route_cfg(top, 1, renormalise=renormalise), dev(r["ids"]),
+                             None if dw is None else dev(dw), dev(r["load"]), balance, 0.0, g)
+            # what has a sigmoid below 2^-126 adds nothing to the chosen weights' part
+            want, tol = ref.route_grad(x, r["ids"], None, dw, r["load"], True, top, renormalise, 1.0, balance,
+                                       0.0, scale, kind)
+            check(("dx", level, scale, with_dw), bd.t, want, tol)
+            if not with_dw and n > 8 and scale > 1:
+                assert np.abs(want).max() > 100 * tol.max()
+            assert b.untouched() and bd.untouched()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("level", [0.0, -20.0, -29.0, -50.0])
+def test_gradient_of_large_factors(mp, kind, level):  # noqa: F811
+    """A pull near 2^102, which 1 / sum s would take past fp32's range."""
+    rng = gen(63)
+    x = low(rng, level, 9, 60, kind)
+    r = ref.route(x, None, None, True, 4)
+    b, bd, scale = Buf(9, 60, kind, init=x), Buf(9, 60, kind), 2.0 ** 112
+    g = mp.logits_grad(bd.t, 1.0, dev_scale=dev(np.float32([scale])))
+    balance = float(np.float32(0.01))
+    mp.mp_route_grad(mp.logits(b.t), None, mp.route_cfg(4, 1), dev(r["ids"]), None,
+                     dev(r["load"]), balance, 0.0, g)
+    want, tol = ref.route_grad(x, r["ids"], None, None, r["load"], True, 4, True, 1.0, balance, 0.0, scale, kind)
+    assert 2.0 ** 90 < np.abs(want).max() < 2.0 ** 110
+    check("dx", bd.t, want, tol)
+    assert bd.untouched()
