@@ -1124,8 +1124,9 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_bias(RouteBiasArgs a)
     for (int i = 0; i < kRouteWaves; ++i) all += part[i];
     for (int e = threadIdx.x; e < n; e += kRouteThreads) {
         const int64_t off = all - load_of(e) * n;
-        const float step = skip || off == 0 ? 0.0f : off > 0 ? a.speed : -a.speed;
-        a.out[layer * n + e] = a.bias[layer * n + e] + step;
+        const float step = off == 0 ? 0.0f : off > 0 ? a.speed : -a.speed;
+        const float bias = a.bias[layer * n + e];
+        a.out[layer * n + e] = skip ? bias : bias + step;            // (-0 + 0 is 0)
     }
 }
 
