@@ -199,7 +199,7 @@ struct JoinSpace {
 
 // All lanes' shares joined: m valid in all lanes, the sums in the first wave's.
 template <int THREADS>
-__device__ __forceinline__ void join(const Share& a, JoinSpace<THREADS>& l, float& m, float& ref, double& s,
+__device__ __forceinline__ void join(const Share& a, float k, JoinSpace<THREADS>& l, float& m, float& ref, double& s,
                                      double& c)
 {
     constexpr int W = THREADS / kWave;
@@ -208,6 +208,17 @@ __device__ __forceinline__ void join(const Share& a, JoinSpace<THREADS>& l, floa
     ref = a.s != 0.0f ? a.ref : -kRefMost;
     s = static_cast<double>(a.s);
     c = static_cast<double>(a.c);
+    // A reference is its logit's exponent rounded to fp32, and the logit counts as 2^y with y that rounding: what the
+    // exponential's own rounding near 1 adds, 2^-24 or so, may be all of a confident row's entropy.  Put right here, of
+    // the lane's largest logit (2^y to 1e-14).  Where a lane's reference is another's, that one has at least 2^-kSlack
+    // of the largest's share, and the entropy is large beside it.
+    const float y = __builtin_fmaf(a.m, k, -a.ref);
+    if (__builtin_fabsf(y) < 0x1p-10f) {
+        const double t = static_cast<double>(y) * 0.69314718055994531;
+        const double off = 1.0 + t * (1.0 + t * (0.5 + t * (1.0 / 6.0))) - static_cast<double>(exp2_hw(y));
+        s += off;
+        c += off * static_cast<double>(y);
+    }
     join_lanes<kWave>(m, ref, s, c);
     if constexpr (W > 1) {
         const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
@@ -579,7 +590,7 @@ __device__ __forceinline__ PieceStat piece_stat(Share share, const Piece<DT>& p,
     lane_max = share.m;
     PieceStat r;
     float ref;
-    join<THREADS>(share, space, r.m, ref, r.s, r.c);
+    join<THREADS>(share, k.k, space, r.m, ref, r.s, r.c);
     r.ref = static_cast<double>(ref);
     if (!(__builtin_fabsf(r.m * k.k) < kRowMost)) {
         share = Share{};
@@ -588,7 +599,7 @@ __device__ __forceinline__ PieceStat piece_stat(Share share, const Piece<DT>& p,
             const float f[1] = {v};
             add_to(share, f, k.k);
         });
-        join<THREADS>(share, space, r.m, ref, r.s, r.c);
+        join<THREADS>(share, k.k, space, r.m, ref, r.s, r.c);
         r.ref = static_cast<double>(r.m) * static_cast<double>(k.k);
     }
     return r;

@@ -4,8 +4,8 @@ import numpy as np
 import pytest
 
 from loss_rows import near
-from score_rows import borders, chain_of, entries, parts_of, planted, reference
-from test_gpu_losses import Buf, empty, ttype
+from score_rows import U, borders, chain_of, entries, parts_of, planted, reference
+from test_gpu_losses import KINDS, Buf, dev, empty, host, ttype
 from test_gpu_scores import mp  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -177,3 +177,30 @@ def test_split_rows_captured_and_replayed(mp):  # noqa: F811
         for one, two in zip([*eager[:3], *eager[3]], [*outs[i % 2][:3], *outs[i % 2][3]]):
             assert torch.equal(one, two)
     assert ws.untouched()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("V", [1000, 9001])
+def test_entropy_of_confident_rows(mp, kind, V):  # noqa: F811
+    """One logit g above all others, each of which has the share q = e^-g / (1 + (V - 1) e^-g): the entropy is
+    right to a small part of itself.  The lane that has the large one adds up `own` logits in fp32 next to 1:
+    of each it loses at most q or u.  Its sum of y 2^y stands at the rounding of the large one's exponent
+    (at most 2 u g) and at what its other logits add, and is rounded once for each of them.  All other lanes'
+    logits count with an error of 5 u (g + 6.3), in both sums, and the additions; lanes are joined in binary64."""
+    gaps = np.array([8.0, 12.0, 16.0, 20.0, 25.0, 30.0])
+    # the large one among the first vectors of its lane, among the last, in a head and in a tail
+    for place in (3, 8 * 64 - 1, V // 2, V - 9, V - 1):
+        x = np.zeros((len(gaps), V))
+        x[:, place] = gaps
+        b = Buf(len(gaps), V, kind, 0, 1, x)
+        lp, lse, H, _ = run(mp, b, 1.0, 0, None, dev(np.full(len(gaps), place)))
+        chain = chain_of(V, kind, len(gaps), 0, False)
+        own = round(chain / U)
+        eps = (V - 1) * np.exp(-gaps)
+        q = np.exp(-gaps) / (1 + eps)
+        want = np.log1p(eps) + (V - 1) * q * gaps
+        tol = (own * np.minimum(q, U) + own * U * (2 * U * gaps + own * q * (gaps + 5.6))
+               + want * (10 * U * (gaps + 6.3) + 2 * chain + 2 * U) + 2.0 ** -50)
+        off = np.abs(host(H) - want)
+        assert (off <= tol).all(), (place, off / tol)
+        assert (tol < want / 20).all()
