@@ -917,19 +917,23 @@ int pairs_per_slot(int vecs)
     return per > 0 ? per : 1;
 }
 
-// Without lists, five workgroups of 256 lanes on a compute unit (this much shared memory each, unused):
-// with eight, 2048 rows would all be there at once, and where a third of them is switched off
-// some units would have eight live ones and others three.  2048 x 128256 bf16, 0.3 off, 68 us
-// against 74; 8192 x 128256 287 either way, 4096 x 50304 65.
+// Without lists, at 7 to 8 rows a compute unit: only five workgroups of 256 lanes fit on one, by shared memory that
+// nothing uses.  With eight, all rows are there at once, and where some are switched off a unit may have eight live ones
+// and another three.  bf16, five against eight: 2048 x 128256 all live 82 us against 85, 0.3 off 67 against 71;
+// 1920 x 50304 34.4 against 36.3 and 28.0 against 30.4.  With fewer rows the rest of a second turn costs more (1281 x
+// 128256 63 against 56; 1664 70 against 70), and with more, eight take turns too (2300 x 128256 100 against 98,
+// 4096 x 32001 fp32 84 against 81).
 constexpr unsigned kReserved = 32000;
+constexpr int kComputeUnits = 256;
 
 template <int DT, int THREADS>
 void whole_rows(const ScoreArgs& a, hipStream_t s)
 {
     const unsigned rows = static_cast<unsigned>(a.x.rows);
     const int per = pairs_per_slot<THREADS>(a.x.vocab / Fmt<DT>::E);
+    const bool apart = THREADS == 256 && a.x.rows > 7 * kComputeUnits && a.x.rows <= 8 * kComputeUnits;
     if (a.top > 0) k_scores<DT, THREADS, true><<<rows, THREADS, 0, s>>>(a, per);
-    else k_scores<DT, THREADS, false><<<rows, THREADS, THREADS == 256 ? kReserved : 0, s>>>(a, per);
+    else k_scores<DT, THREADS, false><<<rows, THREADS, apart ? kReserved : 0, s>>>(a, per);
 }
 
 // Rows of at least kSplitVecs vectors, up to kSplitRows of them.  A call, 20 entries, split against whole:

@@ -204,3 +204,22 @@ def test_entropy_of_confident_rows(mp, kind, V):  # noqa: F811
         off = np.abs(host(H) - want)
         assert (off <= tol).all(), (place, off / tol)
         assert (tol < want / 20).all()
+
+
+@pytest.mark.parametrize("kind,V", [("bf16", 9001), ("fp32", 20001)])
+@pytest.mark.parametrize("rows", [1281, 1792, 1793, 2047, 2048, 2049])
+def test_rows_in_one_turn_and_in_two(mp, kind, V, rows):  # noqa: F811
+    """Without lists, about the number of rows that the chip holds at once."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    b = Buf(rows, V, kind)
+    b.t.copy_(torch.randn(rows, V, generator=g, device="cuda") * 2)
+    t = torch.randint(V, (rows,), generator=g, device="cuda")
+    t[3::5] = -100
+    got = run(mp, b, 1.0, 0, None, t)
+    live = t >= 0
+    assert not any(v[~live].any() for v in got[:3])
+    some = torch.cat([torch.arange(0, rows, 61, device="cuda"), torch.arange(rows - 9, rows, device="cuda")])
+    some = some[live[some]]
+    check_rows(got, b.t[some], t[some], 1.0, chain_of(V, kind, rows, 0, False), 0, some)
+    assert b.untouched()
