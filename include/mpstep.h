@@ -710,7 +710,8 @@ typedef struct {
  *   entropy[r] = -sum_j q_rj log q_rj                  (q = 0 adds 0)
  * and the `top` entries of the largest logits, the largest first and of equal ones
  * (-0 and 0 are equal) the lowest id first: top_ids, their log-probabilities
- * top_logp and the logits themselves, top_values (fp32 holds all three formats).
+ * top_logp and the logits themselves, top_values (fp32 holds all three formats; -0
+ * comes as 0).
  * A logit of -inf is no entry.  Where a row has fewer entries than `top`, the
  * rest have id -1 and value and log-probability -inf; so have all of a
  * switched-off row (its logp, lse and entropy are 0) and of a row without a
@@ -722,7 +723,8 @@ typedef struct {
  *
  * Sums over a row are fp32 in a lane and joined in binary64: lse, entropy and log-probabilities
  * have absolute errors like the losses' (a few 2^-24, more in proportion to the row's
- * length); an entropy is at least 0.  The order of the entries is exact. */
+ * length); an entropy is at least 0, and keeps its leading digits where one entry of ordinary
+ * size has nearly all of the probability.  The order of the entries is exact. */
 mp_status mp_token_score(const mp_logits* x, const int64_t* targets, const mp_score* out,
                          mp_stream stream);
 
@@ -730,8 +732,9 @@ mp_status mp_token_score(const mp_logits* x, const int64_t* targets, const mp_sc
  * dentropy, from the lse and entropy of mp_token_score on the same logits:
  *   dx_rj = scale/T * (dlogp[r] * ((j = t) - q_rj) - dentropy[r] * q_rj (log q_rj + H_r)).
  * dlogp (with targets) or dentropy (with entropy) may be NULL, for none of that
- * part; targets may be given without dlogp, to switch rows off.  A row where both
- * are 0 is written as zeros without being read.  An element with q_rj = 0 takes
+ * part; targets may be given without dlogp, to switch rows off (a target >= vocab makes its
+ * row NaN then too, as in the losses).  A row where both are 0 is written as zeros without being
+ * read.  An element with q_rj = 0 takes
  * none of the entropy's part.  q is as exact as in mp_token_logprob_grad. */
 mp_status mp_token_score_grad(const mp_logits* x, const int64_t* targets, const float* lse,
                               const float* entropy, const float* dlogp, const float* dentropy,
@@ -776,7 +779,10 @@ typedef struct {
  * got, then how many tokens were routed; share, experts fp32: the mean over these
  * tokens of p = s (softmax) or s / sum s (sigmoid); aux, 2 fp32: the losses
  * balance = experts sum_e load_e share_e / (top load[experts]) and the mean of
- * lse^2 (0 for sigmoid scores).  workspace: with load, MP_ROUTE_WORKSPACE_BYTES of
+ * lse^2 (0 for sigmoid scores).  A lane adds up its tokens' shares in fp32 (8 of them at
+ * 65536 x 256, at most 3100), without a bias also its 8 or 16 exponentials of a token, of which
+ * shares, lse and a softmax's undivided weights are formed; lanes are joined in binary64.
+ * workspace: with load, MP_ROUTE_WORKSPACE_BYTES of
  * device memory, 16-byte aligned, used as the losses use theirs. */
 typedef struct {
     float* weights;
@@ -809,8 +815,8 @@ mp_status mp_route(const mp_logits* x, const float* bias, const uint8_t* mask,
  * a token without one has a gradient of 0, or NaN without a distribution.  An id
  * >= experts makes the token's gradient NaN, and no memory is read there; an id that
  * comes twice counts twice.  z_coef must be 0 with sigmoid scores.  Formed in
- * fp32, with sums over a token in binary64, and rounded once.  A sigmoid below 2^-126
- * is 0 (of a token whose logits are all below -32 the balance loss takes shares to
+ * fp32, a lane's sums over its 8 or 16 experts too, which are joined in binary64, and
+ * rounded once.  A sigmoid below 2^-126 is 0 (of a token whose logits are all below -32 the balance loss takes shares to
  * 2^-1000, as mp_route). */
 mp_status mp_route_grad(const mp_logits* x, const uint8_t* mask, const mp_route_cfg* cfg,
                         const int64_t* ids, const float* dweights, const int64_t* load,

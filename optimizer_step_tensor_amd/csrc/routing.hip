@@ -388,9 +388,10 @@ __host__ __device__ __forceinline__ int group_keys(int n, int groups, int all)
 // L lanes per token, P experts a lane: expert (c L + lane) 8 + j is the lane's P's c 8 + j.
 // Bound by the vector units.  131072 x 128 bf16, 8 of 128 by logits: 17 us against 7 us for reads and
 // writes; of some 460 instructions for 16 experts a lane 206 sort.  65536 x 256 bf16, 8 of 256 by a bias in 4
-// of 8 groups, with sums: 58 us, 82 instructions an expert, of which the binary64 score is 32; two
-// waves a SIMD, all that 16 experts' keys leave room for, keep the units at work two thirds of the
-// time.  (Eight experts a lane and four waves: 64 us without sums, 52 with 16.)  7 x 64: 3.2 us, a launch.
+// of 8 groups, with sums: 62 us, 84 instructions an expert, of which the binary64 score is 32; two
+// waves a SIMD, all that 16 experts' keys leave room for, keep the units at work 70 of 100 cycles.  (The same
+// without sums: 43 us; 60 with eight experts and twice the lanes a token, whose joins cost more than two more waves
+// give.)  7 x 64: 2.5 us, a launch.
 template <int DT, int L, int P, int K, bool EXACT, bool SUMS>
 __global__ __launch_bounds__(kRouteThreads, (route_waves<DT, L, P, EXACT, SUMS>()))
 void k_route(RouteArgs a, RouteSums w, int space_bytes)
@@ -418,7 +419,7 @@ void k_route(RouteArgs a, RouteSums w, int space_bytes)
     uint8_t* const open_of = reinterpret_cast<uint8_t*>(reinterpret_cast<Key*>(own_space) + R * (keys + a.groups)) +
                              slot * a.groups;
     // A lane's sums are fp32 (binary64 ones would take sixteen registers more than there are), of 2^22 tokens
-    // over at least 1364 waves: below 3100 additions, 2^-12.4 relative if all were off the same way.
+    // over at least 1360 waves: below 3100 additions, 2^-12.4 relative if all were off the same way.
     // The lanes' are joined in binary64.
     float total[P] = {};
     double squares = 0.0;
@@ -887,9 +888,9 @@ __global__ __launch_bounds__(kFinishThreads) void k_route_finish(RouteArgs a, Ro
 //   softmax  dx_e = s_e (pull_e + ds_e - sum_j s_j (pull_j + ds_j) + 2 F z lse)
 //   sigmoid  dx_e = s_e (1 - s_e) ((pull_e - sum_j p_j pull_j) / sum s + ds_e),    p = s / sum s.
 // (of a token whose logits are all below kLow s and sum s are relative to its largest one's, and ds is scaled instead).
-// L lanes per token and P experts a lane, as in the choice.  fp32 but for the sums over a token: nothing here is
-// compared.  65536 x 256 bf16 by sigmoid: 25 us, 2.7 TB/s read and written; the vector units are at
-// work 70 of 100 cycles, two of 33 instructions an expert being an exponential and a reciprocal.
+// L lanes per token and P experts a lane, as in the choice.  fp32, a lane's sums over its experts too (nothing here is
+// compared), which are joined in binary64.  65536 x 256 bf16 by sigmoid: 26 us, 2.7 TB/s read and written; the vector
+// units are at work 71 of 100 cycles, two of 34 instructions an expert being an exponential and a reciprocal.
 // At most 128 registers, for four waves a SIMD (one kernel would take 130).
 template <int DT, int L, int P, bool SIGMOID>
 __global__ __launch_bounds__(kRouteThreads, 4) void k_route_grad(RouteGradArgs a)
@@ -1141,9 +1142,9 @@ int64_t route_grid(int64_t rows, int lanes, int64_t most)
 template <int DT, int L, int P, int K, bool EXACT>
 void route_shape(const RouteArgs& a, RouteSums& w, hipStream_t s)
 {
-    // As many workgroups as are resident at once: a start costs a wave as much as a tenth of a token's work
-    // (131072 x 128 bf16 18.7 us, 20.3 with a workgroup for every 32 tokens; 65536 x 256 by a bias
-    // 52.9 and 60.1), and with sums each leaves its own.
+    // As many workgroups as are resident at once: a start costs a wave a part of a token's work (131072 x 128
+    // bf16 16.1 us, 16.5 with a workgroup for every 32 tokens; 65536 x 256 by a bias in groups 42.5 and 43.9, without
+    // groups 35.7 and 35.0), and with sums each leaves its own.
     const bool sums = a.load != nullptr;
     int64_t most = 256 * (sums ? route_waves<DT, L, P, EXACT, true>() : route_waves<DT, L, P, EXACT, false>());
     if (sums)

@@ -688,8 +688,9 @@ __global__ __launch_bounds__(THREADS, 8) void k_scores(ScoreArgs a, int per)
 // Few rows, less than the chip has room for: a row is cut into parts, one workgroup each, that leave
 // their sums and their own k largest in the workspace; then one workgroup a row joins them.  A lane
 // holds its vectors of a part, up to kPartHeld: the choice needs no slots and no second read then.
-// Bound by latency, of two launches and of a few dependent steps in each: 1 x 128256 bf16, 20
-// entries, 8 us and 5 us, 48 rows with 8 entries 10 us and 4.5 us, where the reads alone take 0.04 and 1.9 us.
+// Bound by latency: 1 x 128256 bf16 takes 4.0 us and 2.5 us without lists, two launches and the dependent steps of a
+// row's sums; the choice of 20 entries, a bound found bit by bit and barriers, adds as much again (7.8 and 5.1 us).  48
+// rows with 8 entries 10 us and 4.5 us, where the reads alone take 0.04 and 1.9 us.
 constexpr int kPartThreads = 256;
 constexpr int kPartHeld = 4;
 constexpr int kMaxParts = kWave;
@@ -937,9 +938,11 @@ void whole_rows(const ScoreArgs& a, hipStream_t s)
 }
 
 // Rows of at least kSplitVecs vectors, up to kSplitRows of them.  A call, 20 entries, split against whole:
-// 128256 bf16 logits (16032 vectors), 1 row 12.9 us against 18.3, 64 rows 16.0 against 22.7, 128
-// rows 21.2 against 23.6, 200 rows 25.8 against 24.2; 60000 fp32 logits (15000), 1 row 11.5 against 15.3, 128
-// rows 17.5 against 23.3, 300 rows 25.7 against 24.9; 50304 bf16 logits (6288), 1 row 11.5 against 11.3.
+// 128256 bf16 logits (16032 vectors), 1 row 12.9 us against 18.3, 64 rows 15.7 against 19.1, 128 rows 21.0
+// against 21.7, 160 rows 23.3 against 23.2, 200 rows 26.5 against 23.9; 60000 fp32 logits (15000), 1 row 11.5 against
+// 15.3, 128 rows 16.8 against 19.1, 200 rows 21.0 against 24.0, 256 rows 23.7 against 24.4; 262144 bf16 logits, 128 rows 30.5
+// against 37.5, 160 rows 35.0 against 38.2, 200 rows 40.9 against 38.5; 50304 bf16 logits (6288), 1 row 11.5 against 11.3.
+// (Between 128 and 200 rows the shortest of these gain nothing.)
 constexpr int kSplitRows = 128;
 constexpr int kSplitVecs = 10000;
 
@@ -989,6 +992,8 @@ void scores_dt(ScoreArgs a, hipStream_t s)
     // their logits, and for somewhat longer ones where there are enough of them to fill the chip.  bf16, 20
     // entries, 64, 128 and 256 lanes: 8192 x 2000 23, 25 and 40 us, 8192 x 8192 38, 38 and 45, 8192 x 16000
     // 68, 61 and 66, 8192 x 64000 197, 181 and 179; 512 x 8192 11.0, 9.6 and 9.8, 512 x 32000 24, 18 and 14.
+    // At 1024 rows the forms are alike (1024 x 8192 11.1, 10.6 and 11.4, 1024 x 16000 15.6, 13.8 and 14.0), and from there
+    // fewer lanes gain (2048 x 8192 13.7, 13.6 and 15.6, 2048 x 16000 19.0, 19.1 and 20.4).
     // (A bound from 64 lanes' maxima is one for at most 64 entries.)
     const int nvec = a.x.vocab / Fmt<DT>::E;
     const bool many = a.x.rows >= 2048;
